@@ -21,6 +21,9 @@
  *   moe_expert_gelu, moe_forward_gelu         generic experts W2 GELU(W1 u + b1) + b2
  *   moe_backward (_workspace_size), moe_forward_train, moe_backward_saved
  *                                             gradients of the block for training
+ *   moe_residual_norm, moe_residual_norm_backward (_workspace_size)
+ *                                             norms before and after a block, its
+ *                                             gate and residual, and their gradients
  *   moe_get_device_error, moe_route_noalloc_device_error,
  *   moe_forward_gathers_rows, moe_selftest_wait_timeout, moe_status_string
  *
@@ -488,6 +491,74 @@ MOE_API int moe_forward_gathers_rows(const moe_config* cfg, const void* x);
  */
 MOE_API moe_status moe_balance_update(const moe_config* cfg, const int32_t* expert_counts,
                               float* bias, float gamma, float* entropy, void* stream);
+
+/* Settings of the residual norms around a block. All fields are 32-bit. */
+typedef struct {
+  int32_t T;            /* tokens, >= 0                                             */
+  int32_t d;            /* width: a row is a multiple of 16 bytes, at most 32 KiB   */
+  int32_t dtype;        /* moe_dtype of every array                                 */
+  int32_t gate_tokens;  /* >= 1: token t uses gate row t / gate_tokens (1: a row per
+                           token; >= T: one row for all)                            */
+  float eps;            /* > 0, added to the mean square                            */
+  float alpha;          /* residual scale (finite)                                  */
+  float beta;           /* branch scale (finite)                                    */
+  float w_offset;       /* added to every norm weight: 0, or 1 for weights stored
+                           around zero (finite)                                     */
+} moe_norm_config;
+
+/*
+ * moe_residual_norm - the residual step after a block and the norm before the
+ * next one, in one pass.  [DS] eq. 12 (h' = u + MoE(u)), in the form a model
+ * uses it: the block's output may be normalised and gated, the stream scaled.
+ *
+ *   h_out = alpha * h + beta * g . N(y; w_post)
+ *   u     = N(h_out; w_pre)
+ *   N(v; w) = v / sqrt(mean(v^2) + eps) . (w + w_offset)
+ *
+ *   h       [T][d]   the residual stream
+ *   y       [T][d]   the block's output; NULL: no block came before, u = N(h; w_pre)
+ *                    (w_post, gate and h_out must then be NULL; alpha, beta unused)
+ *   w_post  [d]      norm weight of the branch, NULL: y itself
+ *   gate    [ceil(T / gate_tokens)][d]   NULL: 1
+ *   w_pre   [d]      norm weight of the next block's input, NULL: no u
+ *   h_out   [T][d]   OUT; may be h
+ *   u       [T][d]   OUT (NULL exactly if w_pre is); may be y, or h if h_out is not
+ *
+ * Sums are fp32; h_out and u are each rounded once (u from the unrounded
+ * stream). Squares are taken in fp32, so a value past 1.8e19 makes its row's
+ * mean infinite. Arrays overlap only where named. T = 0 enqueues nothing.
+ */
+MOE_API moe_status moe_residual_norm(const moe_norm_config* cfg, const void* h, const void* y,
+                             const void* w_post, const void* gate, const void* w_pre, void* h_out,
+                             void* u, void* stream);
+
+/*
+ * moe_residual_norm_backward - gradients of moe_residual_norm.
+ *
+ *   h_out    [T][d]  the forward's h_out (its h where y is NULL); needed where
+ *                    w_pre is given
+ *   y, w_post, gate, w_pre   as in the forward
+ *   du       [T][d]  gradient of u (NULL exactly if w_pre is)
+ *   dh_out   [T][d]  gradient that reaches h_out by other ways, NULL: none
+ *                    (at least one of du and dh_out is given)
+ *   dh       [T][d]  OUT, NULL: not wanted; may be dh_out
+ *   dy       [T][d]  OUT, NULL: not wanted (or no y); may be du
+ *   dw_post  [d], dgate (gate's shape), dw_pre [d]
+ *                    OUT, each NULL: not wanted; not NULL only where its input is given
+ *
+ * The norms' factors are recomputed from h_out and y. Weight and gate
+ * gradients are summed over tokens in fp32 in a fixed order (the same bits
+ * from call to call) and rounded once. T = 0 zeroes dw_post and dw_pre.
+ * workspace: moe_residual_norm_backward_workspace_size(cfg) bytes, 16-byte
+ * aligned, scratch of this call alone (it holds no error word); 0 bytes where
+ * cfg is invalid. The size depends on the current device's SM count.
+ */
+MOE_API size_t moe_residual_norm_backward_workspace_size(const moe_norm_config* cfg);
+MOE_API moe_status moe_residual_norm_backward(const moe_norm_config* cfg, const void* h_out, const void* y,
+                                      const void* w_post, const void* gate, const void* w_pre,
+                                      const void* du, const void* dh_out, void* dh, void* dy,
+                                      void* dw_post, void* dgate, void* dw_pre, void* workspace,
+                                      size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, reads and clears the workspace's device error word.
  * Returns MOE_OK, MOE_ERR_TIMEOUT (a bounded device wait ran out during an

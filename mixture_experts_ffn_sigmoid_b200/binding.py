@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from .inputs import MoEConfig
+from .inputs import MoEConfig, NormConfig
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_b200.so")
 
@@ -38,7 +38,8 @@ EXPORTED = ("moe_check_config", "moe_workspace_size", "moe_route", "moe_permute"
             "moe_forward_gathers_rows", "moe_route_maps", "moe_route_maps_supported",
             "moe_balance_update",
             "moe_expert_gelu", "moe_forward_gelu", "moe_backward_workspace_size", "moe_backward",
-            "moe_forward_train", "moe_backward_saved", "moe_status_string")
+            "moe_forward_train", "moe_backward_saved", "moe_residual_norm",
+            "moe_residual_norm_backward_workspace_size", "moe_residual_norm_backward", "moe_status_string")
 
 
 class MoEError(RuntimeError):
@@ -53,6 +54,12 @@ class CConfig(ctypes.Structure):
                 ("gate_mode", ctypes.c_int32), ("n_groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("route_scale", ctypes.c_float),
                 ("f_shared", ctypes.c_int32)]
+
+
+class CNormConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate_tokens", ctypes.c_int32), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float), ("w_offset", ctypes.c_float)]
 
 
 _lib = None
@@ -71,7 +78,7 @@ def lib() -> ctypes.CDLL:
                                "`python -m mixture_experts_ffn_sigmoid_b200.build`")
         L = ctypes.CDLL(_LIB_PATH)
         vp, sz, i32p, f32p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p
-        cfgp = ctypes.POINTER(CConfig)
+        cfgp, ncfgp = ctypes.POINTER(CConfig), ctypes.POINTER(CNormConfig)
         sig = {
             "moe_check_config": (ctypes.c_int, [cfgp]),
             "moe_workspace_size": (sz, [cfgp]),
@@ -101,6 +108,10 @@ def lib() -> ctypes.CDLL:
                                                   vp, vp, vp, vp, sz, vp]),
             "moe_backward": (ctypes.c_int, [cfgp, vp, vp, f32p, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                             vp, vp, vp, vp, sz, vp]),
+            "moe_residual_norm": (ctypes.c_int, [ncfgp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "moe_residual_norm_backward_workspace_size": (sz, [ncfgp]),
+            "moe_residual_norm_backward": (ctypes.c_int, [ncfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                          sz, vp]),
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         }
         for name, (res, args) in sig.items():
@@ -490,6 +501,98 @@ def moe_balance_update(cfg, expert_counts, bias, gamma: float, entropy=None, str
     _need(entropy, "entropy", 1, _F32, required=False)
     _check(lib().moe_balance_update(ctypes.byref(c), _ptr(expert_counts), _ptr(bias), float(gamma),
                                     _ptr(entropy), _stream(stream)), "moe_balance_update")
+
+
+# ------------------------------------------------------------ residual norms
+def make_norm_config(cfg: Optional[NormConfig] = None, **kw) -> CNormConfig:
+    """The C struct of a NormConfig, or of one with the given fields."""
+    cfg = NormConfig(**kw) if cfg is None else cfg
+    return CNormConfig(T=cfg.T, d=cfg.d, dtype=_dtype_code(cfg.dtype), gate_tokens=cfg.gate_tokens, eps=cfg.eps,
+                       alpha=cfg.alpha, beta=cfg.beta, w_offset=cfg.w_offset)
+
+
+def _dtype_code(name: str) -> int:
+    if name not in ("f32", "bf16"):
+        raise ValueError(f"dtype {name!r}: expected 'f32' or 'bf16'")
+    return MOE_DTYPE_F32 if name == "f32" else MOE_DTYPE_BF16
+
+
+def _ncfg(c) -> CNormConfig:
+    return c if isinstance(c, CNormConfig) else make_norm_config(c)
+
+
+def _ptrs(*tensors):
+    """Device addresses (None for None) of contiguous CUDA tensors, all on the
+    current device: kernels are launched there, and another GPU's memory may
+    not be reachable from it."""
+    dev = None
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensor must live on a CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"tensor lives on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _need_norm(c: CNormConfig, y, w_post, gate, w_pre):
+    dt, n = _dt(c), c.T * c.d
+    _need(y, "y", n, dt, required=False)
+    _need(w_post, "w_post", c.d, dt, required=False)
+    if gate is not None and c.gate_tokens >= 1:
+        _need(gate, "gate", -(-c.T // c.gate_tokens) * c.d, dt)
+    _need(w_pre, "w_pre", c.d, dt, required=False)
+
+
+def moe_residual_norm(cfg, h, y, w_post, gate, w_pre, h_out, u, stream=None):
+    """h_out = alpha h + beta gate . N(y; w_post) and u = N(h_out; w_pre) in one pass."""
+    c = _ncfg(cfg)
+    dt, n = _dt(c), c.T * c.d
+    _need(h, "h", n, dt)
+    _need_norm(c, y, w_post, gate, w_pre)
+    _need(h_out, "h_out", n, dt, required=y is not None)
+    _need(u, "u", n, dt, required=w_pre is not None)
+    _check(lib().moe_residual_norm(ctypes.byref(c), *_ptrs(h, y, w_post, gate, w_pre, h_out, u), _stream(stream)),
+           "moe_residual_norm")
+
+
+def norm_backward_workspace_size(cfg) -> int:
+    return int(lib().moe_residual_norm_backward_workspace_size(ctypes.byref(_ncfg(cfg))))
+
+
+def alloc_norm_backward_workspace(cfg, device="cuda") -> torch.Tensor:
+    n = norm_backward_workspace_size(cfg)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_residual_norm_backward_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_residual_norm_backward(cfg, h_out, y, w_post, gate, w_pre, du, dh_out, dh, dy, dw_post, dgate, dw_pre,
+                               workspace, stream=None):
+    """Gradients of moe_residual_norm, given those of u and of h_out (None: none)."""
+    c = _ncfg(cfg)
+    dt, n = _dt(c), c.T * c.d
+    _need(h_out, "h_out", n, dt, required=w_pre is not None)
+    _need_norm(c, y, w_post, gate, w_pre)
+    _need(du, "du", n, dt, required=w_pre is not None)
+    for t, name in ((dh_out, "dh_out"), (dh, "dh"), (dy, "dy")):
+        _need(t, name, n, dt, required=False)
+    for t, name in ((dw_post, "dw_post"), (dw_pre, "dw_pre")):
+        _need(t, name, c.d, dt, required=False)
+    if dgate is not None and c.gate_tokens >= 1:
+        _need(dgate, "dgate", -(-c.T // c.gate_tokens) * c.d, dt)
+    _need_ws(workspace)
+    _check(lib().moe_residual_norm_backward(
+        ctypes.byref(c), *_ptrs(h_out, y, w_post, gate, w_pre, du, dh_out, dh, dy, dw_post, dgate, dw_pre, workspace),
+        workspace.numel(), _stream(stream)), "moe_residual_norm_backward")
 
 
 def moe_get_device_error(workspace, stream=None) -> int:

@@ -4,6 +4,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "moe_internal.cuh"
@@ -751,6 +753,20 @@ moe_status enqueue_backward(const moe_config& c, const void* x, const void* w_ro
   return MOE_OK;
 }
 
+// ---- residual norms
+moe_status check_norm_config(const moe_norm_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->T < 0 || c->d <= 0 || c->gate_tokens < 1) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!(c->eps > 0.0f) || !isfinite(c->eps) || !isfinite(c->alpha) || !isfinite(c->beta) || !isfinite(c->w_offset))
+    return MOE_ERR_INVALID_ARG;
+  if (c->d % (c->dtype == MOE_DTYPE_F32 ? 4 : 8)) return MOE_ERR_MISALIGNED;
+  return norm_width_supported(c->dtype, c->d) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+// An optional pointer: NULL or 16-byte aligned.
+moe_status maybe(const void* p) { return p ? need(p) : MOE_OK; }
+
 moe_status clear_error_word(void* ws, cudaStream_t s) {
   MOE_CUDA(cudaMemsetAsync(at<char>(ws, 0), 0, kAlign, s));
   return MOE_OK;
@@ -1243,6 +1259,66 @@ moe_status moe_balance_update(const moe_config* cfg, const int32_t* expert_count
   if (bias && (!(gamma >= 0.0f) || !isfinite(gamma))) return MOE_ERR_INVALID_ARG;
   MOE_CUDA(launch_balance_update(expert_counts, c.E, (long long)c.T * c.k, gamma, bias, entropy,
                                  static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_residual_norm(const moe_norm_config* cfg, const void* h, const void* y, const void* w_post,
+                             const void* gate, const void* w_pre, void* h_out, void* u, void* stream) {
+  TraceRange trace("moe_residual_norm");
+  MOE_TRY(check_norm_config(cfg));
+  const moe_norm_config& c = *cfg;
+  if (!y && (w_post || gate || h_out || !w_pre)) return MOE_ERR_INVALID_ARG;
+  if ((w_pre != nullptr) != (u != nullptr) && c.T > 0) return MOE_ERR_INVALID_ARG;
+  if (c.T == 0) return MOE_OK;
+  MOE_TRY(need(h));
+  MOE_TRY(maybe(y));
+  MOE_TRY(maybe(w_post));
+  MOE_TRY(maybe(gate));
+  MOE_TRY(maybe(w_pre));
+  if (y) MOE_TRY(need(h_out));
+  MOE_TRY(maybe(u));
+  if (u && u == h_out) return MOE_ERR_INVALID_ARG;
+  NormParams p = {c.dtype, c.T, c.d, c.gate_tokens, c.eps, y ? c.alpha : 1.0f, c.beta, c.w_offset,
+                  h, y, w_post, gate, w_pre, h_out, u};
+  MOE_CUDA(launch_residual_norm(p, device_sm_count(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_residual_norm_backward_workspace_size(const moe_norm_config* cfg) {
+  if (check_norm_config(cfg) != MOE_OK) return 0;
+  const int runs = cfg->T > 0 ? norm_backward_runs(cfg->dtype, cfg->T, cfg->d, device_sm_count()) : 1;
+  return (size_t)4 * runs * cfg->d * sizeof(float);
+}
+
+moe_status moe_residual_norm_backward(const moe_norm_config* cfg, const void* h_out, const void* y,
+                                      const void* w_post, const void* gate, const void* w_pre, const void* du,
+                                      const void* dh_out, void* dh, void* dy, void* dw_post, void* dgate,
+                                      void* dw_pre, void* workspace, size_t ws_bytes, void* stream) {
+  TraceRange trace("moe_residual_norm_backward");
+  MOE_TRY(check_norm_config(cfg));
+  const moe_norm_config& c = *cfg;
+  if (!y && (w_post || gate || dy || !w_pre)) return MOE_ERR_INVALID_ARG;
+  if ((dw_post && !w_post) || (dgate && !gate) || (dw_pre && !w_pre)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(workspace));
+  if (ws_bytes < moe_residual_norm_backward_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  MOE_TRY(maybe(dw_post));
+  MOE_TRY(maybe(dw_pre));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c.T == 0) {
+    const size_t bytes = (size_t)c.d * (c.dtype == MOE_DTYPE_F32 ? 4 : 2);
+    if (dw_post) MOE_CUDA(cudaMemsetAsync(dw_post, 0, bytes, s));
+    if (dw_pre) MOE_CUDA(cudaMemsetAsync(dw_pre, 0, bytes, s));
+    return MOE_OK;
+  }
+  if ((w_pre != nullptr) != (du != nullptr) || (!du && !dh_out)) return MOE_ERR_INVALID_ARG;
+  if (w_pre) MOE_TRY(need(h_out));
+  for (const void* q : {y, w_post, gate, w_pre, du, dh_out}) MOE_TRY(maybe(q));
+  for (const void* q : {(const void*)dh, (const void*)dy, (const void*)dgate}) MOE_TRY(maybe(q));
+  if (dh && dh == dy) return MOE_ERR_INVALID_ARG;
+  NormBwdParams p = {c.dtype, c.T, c.d, c.gate_tokens, c.eps, y ? c.alpha : 1.0f, c.beta, c.w_offset,
+                     w_pre ? h_out : nullptr, y, w_post, gate, w_pre, du, dh_out, dh, dy, dw_post, dgate, dw_pre,
+                     static_cast<float*>(workspace)};
+  MOE_CUDA(launch_residual_norm_backward(p, device_sm_count(), s));
   return MOE_OK;
 }
 

@@ -228,6 +228,30 @@ int router_gemm_splits(int T, int E, int K);
 cudaError_t launch_router_gemm(const void* x, const void* w_router, int T, int E, int K, float* partial,
                                int n_split, uint32_t* err, cudaStream_t s);
 
+// Residual norms (norm_kernels.cu). All pointers 16-byte aligned, T > 0.
+struct NormParams {
+  int dtype, T, d, gate_tokens;
+  float eps, alpha, beta, w_offset;
+  const void* h;                    // [T][d]
+  const void* y;                    // [T][d], or null: no branch, u = N(h)
+  const void* w_post;               // [d] or null
+  const void* gate;                 // [ceil(T / gate_tokens)][d] or null
+  const void* w_pre;                // [d] or null
+  void* h_out; void* u;
+};
+struct NormBwdParams {
+  int dtype, T, d, gate_tokens;
+  float eps, alpha, beta, w_offset;
+  const void* h_out; const void* y; const void* w_post; const void* gate; const void* w_pre;
+  const void* du; const void* dh_out;          // each may be null
+  void* dh; void* dy; void* dw_post; void* dgate; void* dw_pre;   // each may be null
+  float* partial;                   // [4][norm_backward_runs()][d]
+};
+bool norm_width_supported(int dtype, int d);
+int norm_backward_runs(int dtype, int T, int d, int num_sms);
+cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s);
+
 int device_sm_count();
 
 }  // namespace moe

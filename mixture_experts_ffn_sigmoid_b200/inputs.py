@@ -83,6 +83,24 @@ class MoEConfig:
         return 2.0 * self.T * (self.E * self.d + routed + shared)
 
 
+@dataclasses.dataclass(frozen=True)
+class NormConfig:
+    """The residual norms around a block: h' = alpha h + beta g . N(y; w_post),
+    u = N(h'; w_pre); ``gate_tokens`` consecutive tokens share a gate row."""
+    T: int
+    d: int
+    dtype: str = "bf16"            # "bf16" or "f32"
+    gate_tokens: int = 1
+    eps: float = 1e-6
+    alpha: float = 1.0
+    beta: float = 1.0
+    w_offset: float = 0.0          # 1.0 for norm weights stored around zero
+
+    @property
+    def n_gates(self) -> int:
+        return -(-self.T // self.gate_tokens)
+
+
 CONFIGS = {
     "tiny_fp32": MoEConfig("tiny_fp32", T=64, d=128, E=8, k=2, f=256, dtype="f32"),
     "mixtral_8x7b": MoEConfig("mixtral_8x7b", T=4096, d=4096, E=8, k=2, f=14336),
