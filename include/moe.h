@@ -21,6 +21,9 @@
  *   moe_expert_gelu, moe_forward_gelu         generic experts W2 GELU(W1 u + b1) + b2
  *   moe_backward (_workspace_size), moe_forward_train, moe_backward_saved
  *                                             gradients of the block for training
+ *   moe_w4_quantize, moe_w4_dequantize, moe_expert_swiglu_w4, moe_forward_w4
+ *                                             the block on 4-bit expert weights, for
+ *                                             decode-sized batches
  *   moe_residual_norm, moe_residual_norm_backward (_workspace_size)
  *                                             norms before and after a block, its
  *                                             gate and residual, and their gradients
@@ -491,6 +494,78 @@ MOE_API int moe_forward_gathers_rows(const moe_config* cfg, const void* x);
  */
 MOE_API moe_status moe_balance_update(const moe_config* cfg, const int32_t* expert_counts,
                               float* bias, float gamma, float* entropy, void* stream);
+
+/* A weight matrix (or a stack of them) of rows of K in 4 bits with group
+ * scales:  W[m][k] = scale[m][k / group] * (code[m][k] - zero[m][k / group]),
+ * group = 32, 64 or 128 dividing K. Rounded nowhere when used: the products run
+ * over code - zero, the scale multiplies each group's fp32 sum. */
+typedef struct {
+  const void* q;       /* [..][K/2] bytes: code of k = 2i in the low four bits, 2i + 1 in the high */
+  const void* scale;   /* [..][K/group] bf16 */
+  const void* zero;    /* [..][K/group] bytes 0..15 (higher bits are ignored); NULL: 8 everywhere */
+} moe_w4_matrix;
+
+/*
+ * moe_w4_quantize - a dense matrix into that form.
+ *
+ *   w       [rows][K]  dtype  16-byte aligned
+ *   out     q, scale and zero receive the result; zero = NULL centres the codes
+ *           on 8 with scale = bf16(max|w| / 7) per group, else scale =
+ *           bf16((max(w, 0) - min(w, 0)) / 15) and zero = round(-min(w, 0) / scale)
+ *
+ * code = round(w / scale) + zero, clamped to 0..15, ties to even, all in fp32.
+ * A group of zeros has scale 0; a group with an infinity or NaN has scale NaN.
+ *
+ * moe_w4_dequantize - the dense values back, rounded to dtype once.
+ *
+ * Both: rows >= 0 (0 enqueues nothing), K a multiple of group; q, scale and w
+ * 16-byte aligned, zero any. They serve any shape stack [..][K] with rows the
+ * product of the leading sizes.
+ */
+MOE_API moe_status moe_w4_quantize(int64_t rows, int32_t K, int32_t dtype, int32_t group, const void* w,
+                           const moe_w4_matrix* out, void* stream);
+MOE_API moe_status moe_w4_dequantize(int64_t rows, int32_t K, int32_t dtype, int32_t group,
+                             const moe_w4_matrix* in, void* w, void* stream);
+
+/*
+ * moe_expert_swiglu_w4 - moe_expert_swiglu on 4-bit weights, for batches in
+ * which an expert sees few rows (decode).  [DS] SwiGLU equation.
+ *
+ *   x              with perm_src: [T][d] bf16, packed row r is x[perm_src[r]];
+ *                  without: [T*k][d], the packed rows
+ *   perm_src       [T*k] int32 or NULL; an entry outside [0, T) reads row 0 and
+ *                  sets MOE_ERR_INVALID_ARG in the error word
+ *   expert_offsets [E+1] int32
+ *   w1, w3         [E][f][d] (K = d), w2 [E][d][f] (K = f)
+ *   x_shared       [T][d] bf16, ws1, ws3 [f_shared][d], ws2 [d][f_shared]
+ *                  (NULL if f_shared == 0)
+ *   y_perm         [T*k][d] bf16 OUT, y_shared [T][d] bf16 OUT (NULL if f_shared == 0)
+ *
+ * bf16 rows only, d, f and f_shared multiples of group, else
+ * MOE_ERR_UNSUPPORTED. The SwiGLU intermediate is rounded to bf16 once, as in
+ * moe_expert_swiglu. Any T is computed; the weights of an expert are read
+ * again for every 8 to 32 of its rows, so long batches belong to
+ * moe_expert_swiglu. Rows of y_perm that no segment covers are left as they
+ * were.
+ */
+MOE_API moe_status moe_expert_swiglu_w4(const moe_config* cfg, int32_t group, const void* x,
+                                const int32_t* perm_src, const int32_t* expert_offsets,
+                                const moe_w4_matrix* w1, const moe_w4_matrix* w3,
+                                const moe_w4_matrix* w2, const void* x_shared,
+                                const moe_w4_matrix* ws1, const moe_w4_matrix* ws3,
+                                const moe_w4_matrix* ws2, void* y_perm, void* y_shared,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * moe_forward_w4 - the whole block (as moe_forward) on 4-bit expert weights:
+ * route, row maps, moe_expert_swiglu_w4 on rows gathered from x, combine. The
+ * router's weights stay bf16. Arguments as above.
+ */
+MOE_API moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, const void* w_router,
+                          const float* bias, const moe_w4_matrix* w1, const moe_w4_matrix* w3,
+                          const moe_w4_matrix* w2, const moe_w4_matrix* ws1, const moe_w4_matrix* ws3,
+                          const moe_w4_matrix* ws2, void* y, void* workspace, size_t ws_bytes,
+                          void* stream);
 
 /* Settings of the residual norms around a block. All fields are 32-bit. */
 typedef struct {

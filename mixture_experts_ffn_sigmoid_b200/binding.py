@@ -38,7 +38,8 @@ EXPORTED = ("moe_check_config", "moe_workspace_size", "moe_route", "moe_permute"
             "moe_forward_gathers_rows", "moe_route_maps", "moe_route_maps_supported",
             "moe_balance_update",
             "moe_expert_gelu", "moe_forward_gelu", "moe_backward_workspace_size", "moe_backward",
-            "moe_forward_train", "moe_backward_saved", "moe_residual_norm",
+            "moe_forward_train", "moe_backward_saved", "moe_w4_quantize", "moe_w4_dequantize",
+            "moe_expert_swiglu_w4", "moe_forward_w4", "moe_residual_norm",
             "moe_residual_norm_backward_workspace_size", "moe_residual_norm_backward", "moe_status_string")
 
 
@@ -54,6 +55,10 @@ class CConfig(ctypes.Structure):
                 ("gate_mode", ctypes.c_int32), ("n_groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("route_scale", ctypes.c_float),
                 ("f_shared", ctypes.c_int32)]
+
+
+class CW4Matrix(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
 
 
 class CNormConfig(ctypes.Structure):
@@ -79,6 +84,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(_LIB_PATH)
         vp, sz, i32p, f32p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p
         cfgp, ncfgp = ctypes.POINTER(CConfig), ctypes.POINTER(CNormConfig)
+        w4p, i32, i64 = ctypes.POINTER(CW4Matrix), ctypes.c_int32, ctypes.c_int64
         sig = {
             "moe_check_config": (ctypes.c_int, [cfgp]),
             "moe_workspace_size": (sz, [cfgp]),
@@ -108,6 +114,11 @@ def lib() -> ctypes.CDLL:
                                                   vp, vp, vp, vp, sz, vp]),
             "moe_backward": (ctypes.c_int, [cfgp, vp, vp, f32p, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                             vp, vp, vp, vp, sz, vp]),
+            "moe_w4_quantize": (ctypes.c_int, [i64, i32, i32, i32, vp, w4p, vp]),
+            "moe_w4_dequantize": (ctypes.c_int, [i64, i32, i32, i32, w4p, vp, vp]),
+            "moe_expert_swiglu_w4": (ctypes.c_int, [cfgp, i32, vp, i32p, i32p, w4p, w4p, w4p, vp, w4p, w4p, w4p, vp,
+                                                    vp, vp, sz, vp]),
+            "moe_forward_w4": (ctypes.c_int, [cfgp, i32, vp, vp, f32p, w4p, w4p, w4p, w4p, w4p, w4p, vp, vp, sz, vp]),
             "moe_residual_norm": (ctypes.c_int, [ncfgp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "moe_residual_norm_backward_workspace_size": (sz, [ncfgp]),
             "moe_residual_norm_backward": (ctypes.c_int, [ncfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
@@ -503,6 +514,135 @@ def moe_balance_update(cfg, expert_counts, bias, gamma: float, entropy=None, str
                                     _ptr(entropy), _stream(stream)), "moe_balance_update")
 
 
+# ------------------------------------------------------------- 4-bit weights
+class W4Matrix:
+    """A weight matrix (or stack of them) [..., K] in 4 bits with group scales:
+    ``q`` uint8 [..., K/2] (even k in the low four bits), ``scale`` bf16
+    [..., K/group], ``zero`` uint8 [..., K/group] or None for 8 everywhere.
+    ``W = scale * (code - zero)``."""
+
+    def __init__(self, q, scale, zero=None, group: int = 128):
+        _need(q, "q", 0, _U8)
+        _need(scale, "scale", 0, torch.bfloat16)
+        _need(zero, "zero", 0, _U8, required=False)
+        if group not in (32, 64, 128):
+            raise ValueError(f"group {group}: expected 32, 64 or 128")
+        if q.dim() < 1 or (2 * q.shape[-1]) % group:
+            raise ValueError(f"q: rows of {2 * q.shape[-1] if q.dim() else 0} codes are not whole groups of {group}")
+        self.q, self.scale, self.zero, self.group = q, scale, zero, group
+        self.K = 2 * q.shape[-1]
+        self.rows = q.numel() // q.shape[-1] if q.numel() else 0
+        for t, name in ((scale, "scale"), (zero, "zero")):
+            if t is not None and t.numel() != self.rows * (self.K // group):
+                raise ValueError(f"{name}: {t.numel()} elements, expected {self.rows * (self.K // group)}")
+
+    @classmethod
+    def empty(cls, *shape, group: int = 128, zero_points: bool = False, device="cuda") -> "W4Matrix":
+        """Uninitialised buffers for a matrix (stack) of the given dense shape."""
+        *lead, K = shape
+        if group not in (32, 64, 128) or K % group:
+            raise ValueError(f"rows of {K} are not whole groups of {group}")
+        return cls(torch.empty(*lead, K // 2, dtype=_U8, device=device),
+                   torch.empty(*lead, K // group, dtype=torch.bfloat16, device=device),
+                   torch.empty(*lead, K // group, dtype=_U8, device=device) if zero_points else None, group)
+
+    @classmethod
+    def quantize(cls, w: torch.Tensor, group: int = 128, zero_points: bool = False, stream=None) -> "W4Matrix":
+        """The 4-bit form of a dense bf16 or fp32 matrix (stack)."""
+        m = cls.empty(*w.shape, group=group, zero_points=zero_points, device=w.device)
+        moe_w4_quantize(w, m, stream)
+        return m
+
+    def _c(self) -> CW4Matrix:
+        return CW4Matrix(*_ptrs(self.q, self.scale, self.zero))
+
+
+def _dense_code(w, name: str) -> int:
+    _need_tensor(w, name)
+    if w.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: dtype {w.dtype}, expected float32 or bfloat16")
+    return MOE_DTYPE_F32 if w.dtype == torch.float32 else MOE_DTYPE_BF16
+
+
+def _need_tensor(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, not {type(t).__name__}")
+
+
+def moe_w4_quantize(w, out: W4Matrix, stream=None):
+    """Write the 4-bit form of the dense matrix w into out (zero points if it has room for them)."""
+    code = _dense_code(w, "w")
+    if w.numel() != out.rows * out.K:
+        raise ValueError(f"w: {w.numel()} elements, out holds {out.rows * out.K}")
+    (pw,) = _ptrs(w)
+    _check(lib().moe_w4_quantize(out.rows, out.K, code, out.group, pw, ctypes.byref(out._c()), _stream(stream)),
+           "moe_w4_quantize")
+
+
+def moe_w4_dequantize(m: W4Matrix, w, stream=None):
+    """Write the dense values of m into w (bf16 or fp32)."""
+    code = _dense_code(w, "w")
+    if w.numel() != m.rows * m.K:
+        raise ValueError(f"w: {w.numel()} elements, m holds {m.rows * m.K}")
+    (pw,) = _ptrs(w)
+    _check(lib().moe_w4_dequantize(m.rows, m.K, code, m.group, ctypes.byref(m._c()), pw, _stream(stream)),
+           "moe_w4_dequantize")
+
+
+def _w4_args(c: CConfig, w1, w3, w2, ws1, ws3, ws2):
+    """The group size and the C structs of a block's 4-bit weights, checked."""
+    sh = c.f_shared > 0
+    out, group = [], None
+    for m, name, rows, K, required in ((w1, "w1", c.E * c.f, c.d, True), (w3, "w3", c.E * c.f, c.d, True),
+                                       (w2, "w2", c.E * c.d, c.f, True), (ws1, "ws1", c.f_shared, c.d, sh),
+                                       (ws3, "ws3", c.f_shared, c.d, sh), (ws2, "ws2", c.d, c.f_shared, sh)):
+        if not required:
+            out.append(None)
+            continue
+        if not isinstance(m, W4Matrix):
+            raise TypeError(f"{name} must be a W4Matrix, not {type(m).__name__}")
+        if m.K != K or m.rows < rows:
+            raise ValueError(f"{name}: {m.rows} rows of {m.K}, needs {rows} rows of {K}")
+        if group is not None and m.group != group:
+            raise ValueError(f"{name}: group {m.group}, the others have {group}")
+        group = m.group
+        out.append(m)
+    return group, [None if m is None else ctypes.byref(m._c()) for m in out]
+
+
+def moe_expert_swiglu_w4(cfg, x, perm_src, expert_offsets, w1, w3, w2, x_shared, ws1, ws3, ws2, y_perm, y_shared,
+                         workspace, stream=None):
+    """moe_expert_swiglu on 4-bit weights (W4Matrix); rows gathered from x by perm_src, or packed if it is None."""
+    c = _cfg(cfg)
+    R, dt, sh = c.T * c.k, _dt(c), c.f_shared > 0
+    _need(x, "x", (R if perm_src is None else c.T) * c.d, dt)
+    _need(perm_src, "perm_src", R, _I32, required=False)
+    _need(expert_offsets, "expert_offsets", c.E + 1, _I32)
+    _need(x_shared, "x_shared", c.T * c.d, dt, required=sh)
+    _need(y_perm, "y_perm", R * c.d, dt)
+    _need(y_shared, "y_shared", c.T * c.d, dt, required=sh)
+    _need_ws(workspace)
+    group, (a1, a3, a2, s1, s3, s2) = _w4_args(c, w1, w3, w2, ws1, ws3, ws2)
+    px, pp, po, pxs, py, pys, pw = _ptrs(x, perm_src, expert_offsets, x_shared, y_perm, y_shared, workspace)
+    _check(lib().moe_expert_swiglu_w4(ctypes.byref(c), group, px, pp, po, a1, a3, a2, pxs, s1, s3, s2, py, pys, pw,
+                                      workspace.numel(), _stream(stream)), "moe_expert_swiglu_w4")
+
+
+def moe_forward_w4(cfg, x, w_router, bias, w1, w3, w2, ws1, ws3, ws2, y, workspace, stream=None):
+    """The block on 4-bit expert weights (W4Matrix); the router's weights are bf16."""
+    c = _cfg(cfg)
+    dt = _dt(c)
+    _need(x, "x", c.T * c.d, dt)
+    _need(w_router, "w_router", c.E * c.d, dt)
+    _need(bias, "bias", c.E, _F32, required=False)
+    _need(y, "y", c.T * c.d, dt)
+    _need_ws(workspace)
+    group, (a1, a3, a2, s1, s3, s2) = _w4_args(c, w1, w3, w2, ws1, ws3, ws2)
+    px, pr, pb, py, pw = _ptrs(x, w_router, bias, y, workspace)
+    _check(lib().moe_forward_w4(ctypes.byref(c), group, px, pr, pb, a1, a3, a2, s1, s3, s2, py, pw,
+                                workspace.numel(), _stream(stream)), "moe_forward_w4")
+
+
 # ------------------------------------------------------------ residual norms
 def make_norm_config(cfg: Optional[NormConfig] = None, **kw) -> CNormConfig:
     """The C struct of a NormConfig, or of one with the given fields."""
@@ -610,7 +750,8 @@ class MoEBlock:
     """Convenience wrapper holding one block's weights and workspace on the GPU.
 
     ``forward(x)`` returns a new ``[T, d]`` tensor (shared + routed, no
-    residual) computed by ``moe_forward``.
+    residual) computed by ``moe_forward``, or by ``moe_forward_w4`` where the
+    expert weights are ``W4Matrix``.
     """
 
     def __init__(self, cfg: MoEConfig, weights: dict, device="cuda"):
@@ -629,6 +770,7 @@ class MoEBlock:
         if out is None:
             out = torch.empty_like(x)
         w = self.w
-        moe_forward(make_config(self.cfg, T), x, w["w_router"], w.get("bias"), w["w1"], w["w3"], w["w2"],
-                    w.get("ws1"), w.get("ws3"), w.get("ws2"), out, self.workspace(T), stream)
+        run = moe_forward_w4 if isinstance(w["w1"], W4Matrix) else moe_forward
+        run(make_config(self.cfg, T), x, w["w_router"], w.get("bias"), w["w1"], w["w3"], w["w2"],
+            w.get("ws1"), w.get("ws3"), w.get("ws2"), out, self.workspace(T), stream)
         return out

@@ -753,6 +753,94 @@ moe_status enqueue_backward(const moe_config& c, const void* x, const void* w_ro
   return MOE_OK;
 }
 
+// ---- 4-bit weights
+bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
+
+// A 4-bit matrix: q and scale 16-byte aligned, zero NULL or anywhere.
+moe_status need_w4(const moe_w4_matrix* m) {
+  if (!m) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(need(m->q));
+  return need(m->scale);
+}
+W4Operand w4_operand(const moe_w4_matrix* m) {
+  return {static_cast<const uint8_t*>(m->q), m->scale, static_cast<const uint8_t*>(m->zero)};
+}
+
+moe_status check_w4_matrix(int64_t rows, int K, int dtype, int group) {
+  if (rows < 0 || K <= 0 || !w4_group_ok(group) || K % group) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  return rows > (int64_t{1} << 62) / K ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status check_w4(const moe_config& c, int group) {
+  if (!w4_group_ok(group)) return MOE_ERR_INVALID_ARG;
+  if (c.dtype != MOE_DTYPE_BF16 || c.d % group || c.f % group || c.f_shared % group) return MOE_ERR_UNSUPPORTED;
+  // Work units (16 weight rows x 8 token rows) are counted in 32 bits.
+  const long long tiles = (c.d > c.f ? c.d : c.f) / 16, rows = (long long)c.T * (c.k + 1) / 8 + c.E + 1;
+  if (tiles * rows > 0x7fffffffLL || (long long)c.T * c.f_shared / 128 > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status need_w4_weights(const moe_config& c, const moe_w4_matrix* w1, const moe_w4_matrix* w3,
+                           const moe_w4_matrix* w2, const moe_w4_matrix* ws1, const moe_w4_matrix* ws3,
+                           const moe_w4_matrix* ws2) {
+  for (const moe_w4_matrix* m : {w1, w3, w2}) MOE_TRY(need_w4(m));
+  if (c.f_shared > 0)
+    for (const moe_w4_matrix* m : {ws1, ws3, ws2}) MOE_TRY(need_w4(m));
+  return MOE_OK;
+}
+
+// Gate/up and down on 4-bit weights. The down launch may start while gate/up
+// drains: it streams its first weights before it waits for h.
+moe_status enqueue_experts_w4(const moe_config& c, int group, const void* x, const int* perm_src, const int* offsets,
+                              const moe_w4_matrix* w1, const moe_w4_matrix* w3, const moe_w4_matrix* w2,
+                              const void* x_sh, const moe_w4_matrix* ws1, const moe_w4_matrix* ws3,
+                              const moe_w4_matrix* ws2, void* y_perm, void* y_sh, void* ws, bool err_keep,
+                              cudaStream_t s) {
+  const Layout L = layout_of(c);
+  const bool shared = c.f_shared > 0;
+  W4GemmParams g = {};
+  g.mats = 2;
+  g.group = group;
+  g.n_routed = c.E;
+  g.offsets = offsets;
+  g.max_rows = c.T * c.k;
+  g.M = c.f; g.K = c.d;
+  g.x = x; g.gather = perm_src; g.gather_rows = c.T;
+  g.out = at<char>(ws, L.h);
+  g.w[0] = w4_operand(w1);
+  g.w[1] = w4_operand(w3);
+  if (shared) {
+    g.dense_rows = c.T; g.M_s = c.f_shared; g.K_s = c.d;
+    g.x_s = x_sh;
+    g.out_s = at<char>(ws, L.h_s);
+    g.w_s[0] = w4_operand(ws1);
+    g.w_s[1] = w4_operand(ws3);
+  }
+  g.err = at<uint32_t>(ws, L.err);
+  g.err_keep = err_keep;
+  MOE_CUDA(launch_w4_gemm(g, device_sm_count(), s));
+  W4GemmParams q = {};
+  q.mats = 1;
+  q.group = group;
+  q.n_routed = c.E;
+  q.offsets = offsets;
+  q.max_rows = g.max_rows;
+  q.M = c.d; q.K = c.f;
+  q.x = g.out;
+  q.out = y_perm;
+  q.w[0] = w4_operand(w2);
+  if (shared) {
+    q.dense_rows = c.T; q.M_s = c.d; q.K_s = c.f_shared;
+    q.x_s = g.out_s;
+    q.out_s = y_sh;
+    q.w_s[0] = w4_operand(ws2);
+  }
+  q.wait_previous = 1;
+  MOE_CUDA(launch_w4_gemm(q, device_sm_count(), s));
+  return MOE_OK;
+}
+
 // ---- residual norms
 moe_status check_norm_config(const moe_norm_config* c) {
   if (!c) return MOE_ERR_INVALID_ARG;
@@ -1259,6 +1347,90 @@ moe_status moe_balance_update(const moe_config* cfg, const int32_t* expert_count
   if (bias && (!(gamma >= 0.0f) || !isfinite(gamma))) return MOE_ERR_INVALID_ARG;
   MOE_CUDA(launch_balance_update(expert_counts, c.E, (long long)c.T * c.k, gamma, bias, entropy,
                                  static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_w4_quantize(int64_t rows, int32_t K, int32_t dtype, int32_t group, const void* w,
+                           const moe_w4_matrix* out, void* stream) {
+  TraceRange trace("moe_w4_quantize");
+  MOE_TRY(check_w4_matrix(rows, K, dtype, group));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(need(w));
+  MOE_TRY(need_w4(out));
+  MOE_CUDA(launch_w4_quantize(dtype, w, rows * K, group, const_cast<void*>(out->q), const_cast<void*>(out->scale),
+                              const_cast<void*>(out->zero), device_sm_count(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_w4_dequantize(int64_t rows, int32_t K, int32_t dtype, int32_t group, const moe_w4_matrix* in, void* w,
+                             void* stream) {
+  TraceRange trace("moe_w4_dequantize");
+  MOE_TRY(check_w4_matrix(rows, K, dtype, group));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(need(w));
+  MOE_TRY(need_w4(in));
+  MOE_CUDA(launch_w4_dequantize(dtype, in->q, in->scale, in->zero, rows * K, group, w, device_sm_count(),
+                                static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_expert_swiglu_w4(const moe_config* cfg, int32_t group, const void* x, const int32_t* perm_src,
+                                const int32_t* expert_offsets, const moe_w4_matrix* w1, const moe_w4_matrix* w3,
+                                const moe_w4_matrix* w2, const void* x_shared, const moe_w4_matrix* ws1,
+                                const moe_w4_matrix* ws3, const moe_w4_matrix* ws2, void* y_perm, void* y_shared,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  TraceRange trace("moe_expert_swiglu_w4");
+  MOE_TRY(check_config(cfg));
+  const moe_config& c = *cfg;
+  MOE_TRY(check_w4(c, group));
+  MOE_TRY(check_ws(c, workspace, ws_bytes));
+  if (c.T == 0) return MOE_OK;
+  MOE_TRY(need(x));
+  if (perm_src) MOE_TRY(need4(perm_src));
+  MOE_TRY(need4(expert_offsets));
+  MOE_TRY(need_w4_weights(c, w1, w3, w2, ws1, ws3, ws2));
+  MOE_TRY(need(y_perm));
+  if (c.f_shared > 0) {
+    MOE_TRY(need(x_shared));
+    MOE_TRY(need(y_shared));
+  }
+  return enqueue_experts_w4(c, group, x, perm_src, expert_offsets, w1, w3, w2, x_shared, ws1, ws3, ws2, y_perm,
+                            y_shared, workspace, false, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, const void* w_router, const float* bias,
+                          const moe_w4_matrix* w1, const moe_w4_matrix* w3, const moe_w4_matrix* w2,
+                          const moe_w4_matrix* ws1, const moe_w4_matrix* ws3, const moe_w4_matrix* ws2, void* y,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  TraceRange trace("moe_forward_w4");
+  MOE_TRY(check_config(cfg));
+  const moe_config& c = *cfg;
+  MOE_TRY(check_w4(c, group));
+  MOE_TRY(check_ws(c, workspace, ws_bytes));
+  if (c.T == 0) return MOE_OK;
+  MOE_TRY(need(x));
+  MOE_TRY(need(w_router));
+  if (bias) MOE_TRY(need4(bias));
+  MOE_TRY(need_w4_weights(c, w1, w3, w2, ws1, ws3, ws2));
+  MOE_TRY(need(y));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Layout L = layout_of(c);
+  void* ws = workspace;
+  MOE_TRY(clear_error_word(ws, s));
+  int* idx = at<int>(ws, L.idx);
+  float* gate = at<float>(ws, L.gate);
+  int* offsets = at<int>(ws, L.offsets);
+  int *inv_row = at<int>(ws, L.inv_row), *perm_src = at<int>(ws, L.perm_src);
+  const bool maps_in_route = route_writes_maps(c);
+  MOE_TRY(enqueue_route(c, x, w_router, bias, idx, gate, at<int>(ws, L.counts), offsets, ws, s,
+                        maps_in_route ? inv_row : nullptr, maps_in_route ? perm_src : nullptr));
+  if (!maps_in_route)
+    MOE_CUDA(launch_permute(c.dtype, x, idx, offsets, at<int>(ws, L.cbase), route_tile_base(c, ws), c.T, c.d, c.E, c.k,
+                            nullptr, perm_src, inv_row, device_sm_count(), s, false, at<uint32_t>(ws, L.err)));
+  void* y_s = c.f_shared > 0 ? at<char>(ws, L.y_s) : nullptr;
+  MOE_TRY(enqueue_experts_w4(c, group, x, perm_src, offsets, w1, w3, w2, x, ws1, ws3, ws2, at<char>(ws, L.y_perm), y_s,
+                             ws, true, s));
+  MOE_CUDA(launch_combine(c.dtype, at<char>(ws, L.y_perm), inv_row, gate, y_s, y, c.T, c.d, c.k, device_sm_count(), s));
   return MOE_OK;
 }
 

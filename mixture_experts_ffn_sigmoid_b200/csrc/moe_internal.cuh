@@ -252,6 +252,30 @@ int norm_backward_runs(int dtype, int T, int d, int num_sms);
 cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s);
 
+// Experts on 4-bit weights (w4_kernels.cu), bf16 rows.
+struct W4Operand {
+  const uint8_t* q; const void* scale; const uint8_t* zero;   // zero: null = 8
+};
+struct W4GemmParams {
+  int mats;                 // 2: out = SiLU(x W0^T) * (x W1^T); 1: out = x W0^T
+  int group;                // 32, 64 or 128; divides K and K_s
+  int n_routed; const int* offsets; int max_rows;
+  int M, K;                 // weight rows per routed expert (a multiple of 32), reduction length
+  const void* x; const int* gather; int gather_rows;   // token rows, or the rows that gather picks
+  void* out;                // [max_rows][M]
+  int dense_rows, M_s, K_s; // the shared expert, 0 rows: none
+  const void* x_s; void* out_s;
+  W4Operand w[2], w_s[2];
+  uint32_t* err;            // or null: no check of offsets and gather
+  int err_keep;             // add to the word what earlier kernels of the call left in it
+  int wait_previous;        // start early, wait for the launch before (programmatic dependence)
+};
+cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_w4_quantize(int dtype, const void* w, long long n, int group, void* q, void* scale, void* zero,
+                               int num_sms, cudaStream_t s);
+cudaError_t launch_w4_dequantize(int dtype, const void* q, const void* scale, const void* zero, long long n, int group,
+                                 void* w, int num_sms, cudaStream_t s);
+
 int device_sm_count();
 
 }  // namespace moe

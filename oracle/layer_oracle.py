@@ -66,3 +66,20 @@ def residual_norm_backward(h_out, y, w_post, gate, w_pre, du, dh_out, *, gate_to
     else:
         out["dy"], out["dw_post"] = rms_norm_backward(y, w_post, dz, eps, w_offset)
     return out
+
+
+# ------------------------------------------------------------ 4-bit weights
+def w4_dense(q, scale, zero, group):
+    """Dense fp64 values of 4-bit codes: q bytes [..., K/2] (even k low), scale
+    and zero [..., K/group], zero None: 8."""
+    code = np.empty((*q.shape[:-1], 2 * q.shape[-1]))
+    code[..., 0::2], code[..., 1::2] = q & 15, q >> 4
+    z = 8.0 if zero is None else np.repeat(zero.astype(np.float64), group, axis=-1)
+    return np.repeat(scale, group, axis=-1) * (code - z)
+
+
+def swiglu_rows(x, w1, w3, w2):
+    """(y, a, b, h) of W2 (SiLU(W1 x) * W3 x) for rows x."""
+    a, b = x @ w1.T, x @ w3.T
+    h = a / (1.0 + np.exp(-a)) * b
+    return h @ w2.T, a, b, h

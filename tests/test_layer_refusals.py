@@ -102,3 +102,117 @@ def test_norm_binding_refuses_short_or_wrong_tensors(name, bad):
     a[name] = bad
     with pytest.raises(ValueError, match=name):
         B.moe_residual_norm(cfg, **a)
+
+
+# ------------------------------------------------------------- 4-bit weights
+def w4(q=FAKE, scale=FAKE, zero=None):
+    return ctypes.byref(B.CW4Matrix(q, scale, zero))
+
+
+@pytest.mark.parametrize("rows,K,dtype,group,status", [
+    (-1, 128, 0, 64, B.MOE_ERR_INVALID_ARG), (4, 0, 0, 64, B.MOE_ERR_INVALID_ARG), (4, 100, 0, 64, B.MOE_ERR_INVALID_ARG),
+    (4, 128, 2, 64, B.MOE_ERR_INVALID_ARG), (4, 128, 0, 16, B.MOE_ERR_INVALID_ARG), (4, 128, 0, 0, B.MOE_ERR_INVALID_ARG),
+    (1 << 60, 128, 0, 64, B.MOE_ERR_UNSUPPORTED), (0, 128, 0, 64, B.MOE_OK)])
+def test_w4_matrix_shapes(rows, K, dtype, group, status):
+    L = B.lib()
+    assert L.moe_w4_quantize(rows, K, dtype, group, FAKE, w4(), None) == status
+    assert L.moe_w4_dequantize(rows, K, dtype, group, w4(), FAKE, None) == status
+
+
+@pytest.mark.parametrize("m,w,status", [
+    (None, FAKE, B.MOE_ERR_INVALID_ARG), (w4(q=None), FAKE, B.MOE_ERR_INVALID_ARG),
+    (w4(scale=None), FAKE, B.MOE_ERR_INVALID_ARG), (w4(q=ODD), FAKE, B.MOE_ERR_MISALIGNED),
+    (w4(scale=ODD), FAKE, B.MOE_ERR_MISALIGNED), (w4(), None, B.MOE_ERR_INVALID_ARG), (w4(), ODD, B.MOE_ERR_MISALIGNED)])
+def test_w4_matrix_pointers(m, w, status):
+    L = B.lib()
+    assert L.moe_w4_quantize(4, 128, 0, 64, w, m, None) == status
+    assert L.moe_w4_dequantize(4, 128, 0, 64, m, w, None) == status
+
+
+def moe_cfg(**kw):
+    return B.CConfig(**{**dict(T=8, d=128, E=4, k=2, f=256, dtype=B.MOE_DTYPE_BF16, gate_mode=0, n_groups=1, topk_groups=1,
+                               route_scale=1.0, f_shared=128), **kw})
+
+
+def call_experts_w4(cfg, group=64, **kw):
+    a = dict(x=FAKE, perm_src=FAKE, off=FAKE, w1=w4(), w3=w4(), w2=w4(), xs=FAKE, ws1=w4(), ws3=w4(), ws2=w4(), y=FAKE,
+             ys=FAKE, ws=FAKE, n=BIG)
+    a.update(kw)
+    return B.lib().moe_expert_swiglu_w4(ctypes.byref(cfg), group, *[a[n] for n in (
+        "x", "perm_src", "off", "w1", "w3", "w2", "xs", "ws1", "ws3", "ws2", "y", "ys", "ws", "n")], None)
+
+
+def call_forward_w4(cfg, group=64, **kw):
+    a = dict(x=FAKE, wr=FAKE, bias=None, w1=w4(), w3=w4(), w2=w4(), ws1=w4(), ws3=w4(), ws2=w4(), y=FAKE, ws=FAKE, n=BIG)
+    a.update(kw)
+    return B.lib().moe_forward_w4(ctypes.byref(cfg), group, *[a[n] for n in (
+        "x", "wr", "bias", "w1", "w3", "w2", "ws1", "ws3", "ws2", "y", "ws", "n")], None)
+
+
+@pytest.mark.parametrize("kw,group,status", [
+    (dict(k=5), 64, B.MOE_ERR_INVALID_ARG), ({}, 16, B.MOE_ERR_INVALID_ARG), ({}, 256, B.MOE_ERR_INVALID_ARG),
+    (dict(dtype=B.MOE_DTYPE_F32), 64, B.MOE_ERR_UNSUPPORTED), (dict(d=96), 64, B.MOE_ERR_UNSUPPORTED),
+    (dict(f=288), 64, B.MOE_ERR_UNSUPPORTED), (dict(f_shared=96), 64, B.MOE_ERR_UNSUPPORTED)])
+def test_w4_experts_settings(kw, group, status):
+    assert call_experts_w4(moe_cfg(**kw), group) == status
+    assert call_forward_w4(moe_cfg(**kw), group) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    *[({n: None}, B.MOE_ERR_INVALID_ARG) for n in ("x", "w1", "w3", "w2", "ws1", "ws3", "ws2", "y", "ws")],
+    (dict(x=ODD), B.MOE_ERR_MISALIGNED), (dict(w2=w4(q=ODD)), B.MOE_ERR_MISALIGNED),
+    (dict(ws1=w4(scale=None)), B.MOE_ERR_INVALID_ARG), (dict(y=ODD), B.MOE_ERR_MISALIGNED),
+    (dict(n=1000), B.MOE_ERR_WORKSPACE_TOO_SMALL)])
+def test_w4_experts_pointers(kw, status):
+    assert call_experts_w4(moe_cfg(), **kw) == status
+    assert call_forward_w4(moe_cfg(), **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(off=None), B.MOE_ERR_INVALID_ARG), (dict(xs=None), B.MOE_ERR_INVALID_ARG), (dict(ys=None), B.MOE_ERR_INVALID_ARG),
+    (dict(off=FAKE + 2), B.MOE_ERR_MISALIGNED), (dict(perm_src=FAKE + 1), B.MOE_ERR_MISALIGNED)])
+def test_w4_expert_tables(kw, status):
+    assert call_experts_w4(moe_cfg(), **kw) == status
+
+
+def test_w4_no_tokens():
+    assert call_experts_w4(moe_cfg(T=0), x=None, y=None) == B.MOE_OK
+    assert call_forward_w4(moe_cfg(T=0), x=None, y=None) == B.MOE_OK
+
+
+def test_w4_matrix_binding():
+    u8 = torch.uint8
+    with pytest.raises(ValueError, match="group"):
+        B.W4Matrix(torch.zeros(4, 64, dtype=u8), torch.zeros(4, 8, dtype=bf), group=16)
+    with pytest.raises(ValueError, match="q"):
+        B.W4Matrix(torch.zeros(4, 64), torch.zeros(4, 2, dtype=bf), group=64)
+    with pytest.raises(ValueError, match="scale"):
+        B.W4Matrix(torch.zeros(4, 64, dtype=u8), torch.zeros(4, 3, dtype=bf), group=64)
+    with pytest.raises(ValueError, match="zero"):
+        B.W4Matrix(torch.zeros(4, 64, dtype=u8), torch.zeros(4, 2, dtype=bf), torch.zeros(4, 1, dtype=u8), group=64)
+    with pytest.raises(ValueError, match="whole groups"):
+        B.W4Matrix.empty(4, 100, group=64, device="cpu")
+    m = B.W4Matrix.empty(4, 128, group=64, zero_points=True, device="cpu")
+    assert (m.rows, m.K, m.zero.shape) == (4, 128, (4, 2))
+    with pytest.raises(ValueError, match="CUDA"):
+        B.moe_w4_quantize(torch.zeros(4, 128), m)
+    with pytest.raises(ValueError, match="elements"):
+        B.moe_w4_quantize(torch.zeros(3, 128), m)
+    with pytest.raises(ValueError, match="dtype"):
+        B.moe_w4_dequantize(m, torch.zeros(4, 128, dtype=torch.float16))
+
+
+def test_w4_block_binding():
+    from mixture_experts_ffn_sigmoid_b200.inputs import MoEConfig
+    cfg = MoEConfig("c", T=2, d=128, E=4, k=2, f=64)
+    make = lambda *s, group=64: B.W4Matrix.empty(*s, group=group, device="cpu")
+    a = dict(x=torch.zeros(2, 128, dtype=bf), w_router=torch.zeros(4, 128, dtype=bf), bias=None, w1=make(4, 64, 128),
+             w3=make(4, 64, 128), w2=make(4, 128, 64), ws1=None, ws3=None, ws2=None, y=torch.zeros(2, 128, dtype=bf),
+             workspace=torch.zeros(8, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="CUDA"):
+        B.moe_forward_w4(cfg, **a)
+    for name, bad in (("w1", make(3, 64, 128)), ("w2", make(4, 64, 128)), ("w3", make(4, 64, 128, group=128))):
+        with pytest.raises(ValueError, match=name):
+            B.moe_forward_w4(cfg, **{**a, name: bad})
+    with pytest.raises(TypeError, match="w1"):
+        B.moe_forward_w4(cfg, **{**a, "w1": torch.zeros(4, 64, 128)})
