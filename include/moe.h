@@ -21,6 +21,9 @@
  *   moe_expert_gelu, moe_forward_gelu         generic experts W2 GELU(W1 u + b1) + b2
  *   moe_backward (_workspace_size), moe_forward_train, moe_backward_saved
  *                                             gradients of the block for training
+ *   moe_orthogonalize, moe_muon_step (moe_ortho_workspace_size)
+ *                                             Newton-Schulz products over weight
+ *                                             gradients: the Muon update
  *   moe_w4_quantize, moe_w4_dequantize, moe_expert_swiglu_w4, moe_forward_w4
  *                                             the block on 4-bit expert weights, for
  *                                             decode-sized batches
@@ -566,6 +569,58 @@ MOE_API moe_status moe_forward_w4(const moe_config* cfg, int32_t group, const vo
                           const moe_w4_matrix* w2, const moe_w4_matrix* ws1, const moe_w4_matrix* ws3,
                           const moe_w4_matrix* ws2, void* y, void* workspace, size_t ws_bytes,
                           void* stream);
+
+/* A stack of matrices to orthogonalise. All fields are 32-bit. */
+typedef struct {
+  int32_t n;            /* matrices, >= 0                                        */
+  int32_t rows, cols;   /* of each, 1..65536, any (odd sizes too)                */
+  int32_t dtype;        /* moe_dtype of g                                        */
+  int32_t steps;        /* Newton-Schulz steps, 1..64                            */
+  float eps;            /* > 0, added to each matrix's Frobenius norm            */
+} moe_ortho_config;
+
+/*
+ * moe_orthogonalize - Newton-Schulz orthogonalisation of every matrix of a
+ * stack, e.g. of moe_backward's dw1 [E][f][d]; the pages have no counterpart.
+ *
+ *   X = g / (|g|_F + eps)                       (of the transpose if rows > cols)
+ *   steps times:  A = X X^T;  X = a X + (b A + c A^2) X
+ *
+ *   coeffs   host array [steps][3] of a, b, c, read during the call; NULL:
+ *            3.4445, -4.7750, 2.0315 in every step
+ *   g        [n][rows][cols]  dtype
+ *   o        [n][rows][cols]  bf16 OUT, whatever dtype is; may be g if that is bf16
+ *
+ * The products run on fp16 operands with fp32 accumulation, each rounded once:
+ * five steps end about 1e-3 of the result's norm from the exact ones, less
+ * than o's own rounding. A matrix of zeros (an expert no token chose) gives
+ * zeros; one with an infinity or NaN gives undefined values in itself only.
+ * Norms are summed in fp32: entries past 1e19 overflow them. Coefficients
+ * under which a singular value in [0, 1] leaves [-8, 8] at any step, or that
+ * are not finite, return MOE_ERR_INVALID_ARG.
+ *
+ * moe_muon_step - the Muon update of a stack of weight matrices:
+ *
+ *   momentum = mu * momentum + g
+ *   U        = g + mu * momentum (nesterov != 0) or momentum
+ *   weight   = (1 - lr * weight_decay) * weight - lr * scale * orthogonalize(U)
+ *
+ *   momentum [n][rows][cols]  fp32 IN/OUT
+ *   weight   [n][rows][cols]  weight_dtype IN/OUT, rounded once
+ *   lr, mu, weight_decay, scale   finite
+ *
+ * Both: every pointer 16-byte aligned; workspace of
+ * moe_ortho_workspace_size(cfg) bytes (0: cfg is not valid). Large stacks are
+ * worked through in groups of matrices, so it grows no further from some n on;
+ * it depends on the current device's SM count. n = 0 enqueues nothing.
+ */
+MOE_API size_t moe_ortho_workspace_size(const moe_ortho_config* cfg);
+MOE_API moe_status moe_orthogonalize(const moe_ortho_config* cfg, const float* coeffs, const void* g, void* o,
+                             void* workspace, size_t ws_bytes, void* stream);
+MOE_API moe_status moe_muon_step(const moe_ortho_config* cfg, const float* coeffs, const void* g,
+                         float* momentum, void* weight, int32_t weight_dtype, float lr, float mu,
+                         int32_t nesterov, float weight_decay, float scale, void* workspace,
+                         size_t ws_bytes, void* stream);
 
 /* Settings of the residual norms around a block. All fields are 32-bit. */
 typedef struct {

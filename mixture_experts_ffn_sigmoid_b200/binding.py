@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from .inputs import MoEConfig, NormConfig
+from .inputs import MoEConfig, NormConfig, OrthoConfig
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_b200.so")
 
@@ -39,7 +39,8 @@ EXPORTED = ("moe_check_config", "moe_workspace_size", "moe_route", "moe_permute"
             "moe_balance_update",
             "moe_expert_gelu", "moe_forward_gelu", "moe_backward_workspace_size", "moe_backward",
             "moe_forward_train", "moe_backward_saved", "moe_w4_quantize", "moe_w4_dequantize",
-            "moe_expert_swiglu_w4", "moe_forward_w4", "moe_residual_norm",
+            "moe_expert_swiglu_w4", "moe_forward_w4", "moe_ortho_workspace_size", "moe_orthogonalize", "moe_muon_step",
+            "moe_residual_norm",
             "moe_residual_norm_backward_workspace_size", "moe_residual_norm_backward", "moe_status_string")
 
 
@@ -59,6 +60,11 @@ class CConfig(ctypes.Structure):
 
 class CW4Matrix(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
+
+
+class COrthoConfig(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class CNormConfig(ctypes.Structure):
@@ -84,7 +90,8 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(_LIB_PATH)
         vp, sz, i32p, f32p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p
         cfgp, ncfgp = ctypes.POINTER(CConfig), ctypes.POINTER(CNormConfig)
-        w4p, i32, i64 = ctypes.POINTER(CW4Matrix), ctypes.c_int32, ctypes.c_int64
+        w4p, ocfgp = ctypes.POINTER(CW4Matrix), ctypes.POINTER(COrthoConfig)
+        i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
         sig = {
             "moe_check_config": (ctypes.c_int, [cfgp]),
             "moe_workspace_size": (sz, [cfgp]),
@@ -114,6 +121,9 @@ def lib() -> ctypes.CDLL:
                                                   vp, vp, vp, vp, sz, vp]),
             "moe_backward": (ctypes.c_int, [cfgp, vp, vp, f32p, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                             vp, vp, vp, vp, sz, vp]),
+            "moe_ortho_workspace_size": (sz, [ocfgp]),
+            "moe_orthogonalize": (ctypes.c_int, [ocfgp, vp, vp, vp, vp, sz, vp]),
+            "moe_muon_step": (ctypes.c_int, [ocfgp, vp, vp, vp, vp, i32, f32, f32, i32, f32, f32, vp, sz, vp]),
             "moe_w4_quantize": (ctypes.c_int, [i64, i32, i32, i32, vp, w4p, vp]),
             "moe_w4_dequantize": (ctypes.c_int, [i64, i32, i32, i32, w4p, vp, vp]),
             "moe_expert_swiglu_w4": (ctypes.c_int, [cfgp, i32, vp, i32p, i32p, w4p, w4p, w4p, vp, w4p, w4p, w4p, vp,
@@ -641,6 +651,71 @@ def moe_forward_w4(cfg, x, w_router, bias, w1, w3, w2, ws1, ws3, ws2, y, workspa
     px, pr, pb, py, pw = _ptrs(x, w_router, bias, y, workspace)
     _check(lib().moe_forward_w4(ctypes.byref(c), group, px, pr, pb, a1, a3, a2, s1, s3, s2, py, pw,
                                 workspace.numel(), _stream(stream)), "moe_forward_w4")
+
+
+# --------------------------------------------------------- orthogonalisation
+def make_ortho_config(cfg: Optional[OrthoConfig] = None, **kw) -> COrthoConfig:
+    """The C struct of an OrthoConfig, or of one with the given fields."""
+    cfg = OrthoConfig(**kw) if cfg is None else cfg
+    return COrthoConfig(n=cfg.n, rows=cfg.rows, cols=cfg.cols, dtype=_dtype_code(cfg.dtype), steps=cfg.steps,
+                        eps=cfg.eps)
+
+
+def _ocfg(c) -> COrthoConfig:
+    return c if isinstance(c, COrthoConfig) else make_ortho_config(c)
+
+
+def ortho_workspace_size(cfg) -> int:
+    return int(lib().moe_ortho_workspace_size(ctypes.byref(_ocfg(cfg))))
+
+
+def alloc_ortho_workspace(cfg, device="cuda") -> torch.Tensor:
+    n = ortho_workspace_size(cfg)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_ortho_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _coeffs(c: COrthoConfig, coeffs):
+    """The host array of a, b, c per step: None for the default, one triple for
+    every step, or a triple for each."""
+    if coeffs is None:
+        return None
+    flat = [float(v) for t in coeffs for v in (t if isinstance(t, (tuple, list)) else (t,))]
+    if len(flat) == 3:
+        flat *= max(c.steps, 1)
+    if len(flat) != 3 * c.steps:
+        raise ValueError(f"coeffs: {len(flat)} numbers, expected 3 or {3 * c.steps}")
+    return (ctypes.c_float * len(flat))(*flat)
+
+
+def moe_orthogonalize(cfg, g, o, workspace, coeffs=None, stream=None):
+    """Newton-Schulz orthogonalisation of every matrix of g [n, rows, cols] into o (bf16)."""
+    c = _ocfg(cfg)
+    n = c.n * c.rows * c.cols
+    _need(g, "g", n, _dt(c))
+    _need(o, "o", n, torch.bfloat16)
+    _need_ws(workspace)
+    abc = _coeffs(c, coeffs)
+    pg, po, pw = _ptrs(g, o, workspace)
+    _check(lib().moe_orthogonalize(ctypes.byref(c), abc, pg, po, pw, workspace.numel(), _stream(stream)),
+           "moe_orthogonalize")
+
+
+def moe_muon_step(cfg, g, momentum, weight, workspace, lr: float, mu: float = 0.95, nesterov: bool = True,
+                  weight_decay: float = 0.0, scale: float = 1.0, coeffs=None, stream=None):
+    """Muon's update in place: momentum (fp32) by g, weight (fp32 or bf16) by the orthogonalised momentum."""
+    c = _ocfg(cfg)
+    n = c.n * c.rows * c.cols
+    code = _dense_code(weight, "weight")
+    _need(g, "g", n, _dt(c))
+    _need(momentum, "momentum", n, _F32)
+    _need(weight, "weight", n, weight.dtype)
+    _need_ws(workspace)
+    abc = _coeffs(c, coeffs)
+    pg, pm, pw, ps = _ptrs(g, momentum, weight, workspace)
+    _check(lib().moe_muon_step(ctypes.byref(c), abc, pg, pm, pw, code, lr, mu, int(nesterov), weight_decay, scale, ps,
+                               workspace.numel(), _stream(stream)), "moe_muon_step")
 
 
 # ------------------------------------------------------------ residual norms

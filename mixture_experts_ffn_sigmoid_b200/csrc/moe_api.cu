@@ -753,6 +753,47 @@ moe_status enqueue_backward(const moe_config& c, const void* x, const void* w_ro
   return MOE_OK;
 }
 
+// ---- orthogonalisation
+moe_status check_ortho_config(const moe_ortho_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->n < 0 || c->rows <= 0 || c->cols <= 0 || c->steps < 1 || c->steps > 64) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!(c->eps > 0.0f) || !isfinite(c->eps)) return MOE_ERR_INVALID_ARG;
+  return c->rows > 65536 || c->cols > 65536 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+constexpr int kMaxOrthoSteps = 64;
+constexpr float kMuonCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
+
+// The steps' coefficients (the caller's or the default) into `out`. The
+// products hold X, A and b A + c A^2 in fp16 times 64: singular values that
+// stay below 8 keep all three far from its largest value. The polynomials are
+// followed over a grid of the first singular values; between its points the
+// margin to overflow (X below 1000, B below 1000) covers them.
+moe_status ortho_coeffs(const moe_ortho_config& c, const float* in, float* out) {
+  for (int k = 0; k < c.steps; ++k)
+    for (int j = 0; j < 3; ++j) out[3 * k + j] = in ? in[3 * k + j] : kMuonCoeffs[j];
+  for (int k = 0; k < 3 * c.steps; ++k)
+    if (!isfinite(out[k])) return MOE_ERR_INVALID_ARG;
+  if (!in) return MOE_OK;      // the default keeps [0, 1] below 1.3 over all 64 steps
+  constexpr int kGrid = 1024;
+  for (int i = 0; i <= kGrid; ++i) {
+    double s = (double)i / kGrid;
+    for (int k = 0; k < c.steps; ++k) {
+      const double s2 = s * s, p = out[3 * k] + out[3 * k + 1] * s2 + out[3 * k + 2] * s2 * s2;
+      if (!(fabs(p) <= 500.0)) return MOE_ERR_INVALID_ARG;
+      s *= p;
+      if (!(fabs(s) <= 8.0)) return MOE_ERR_INVALID_ARG;
+    }
+  }
+  return MOE_OK;
+}
+
+moe_status check_ortho_ws(const moe_ortho_config& c, void* ws, size_t bytes) {
+  MOE_TRY(need(ws));
+  return bytes < ortho_workspace_bytes(c.n, c.rows, c.cols, device_sm_count()) ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
 // ---- 4-bit weights
 bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
 
@@ -1347,6 +1388,64 @@ moe_status moe_balance_update(const moe_config* cfg, const int32_t* expert_count
   if (bias && (!(gamma >= 0.0f) || !isfinite(gamma))) return MOE_ERR_INVALID_ARG;
   MOE_CUDA(launch_balance_update(expert_counts, c.E, (long long)c.T * c.k, gamma, bias, entropy,
                                  static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_ortho_workspace_size(const moe_ortho_config* cfg) {
+  if (check_ortho_config(cfg) != MOE_OK) return 0;
+  return ortho_workspace_bytes(cfg->n, cfg->rows, cfg->cols, device_sm_count());
+}
+
+moe_status moe_orthogonalize(const moe_ortho_config* cfg, const float* coeffs, const void* g, void* o, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  TraceRange trace("moe_orthogonalize");
+  MOE_TRY(check_ortho_config(cfg));
+  const moe_ortho_config& c = *cfg;
+  float abc[3 * kMaxOrthoSteps];
+  MOE_TRY(ortho_coeffs(c, coeffs, abc));
+  MOE_TRY(check_ortho_ws(c, workspace, ws_bytes));
+  if (c.n == 0) return MOE_OK;
+  MOE_TRY(need(g));
+  MOE_TRY(need(o));
+  OrthoParams p = {};
+  p.n = c.n; p.rows = c.rows; p.cols = c.cols; p.dtype = c.dtype; p.steps = c.steps;
+  p.eps = c.eps;
+  p.coeffs = abc;
+  p.g = g;
+  p.o = o;
+  MOE_CUDA(launch_ortho(p, workspace, device_sm_count(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_muon_step(const moe_ortho_config* cfg, const float* coeffs, const void* g, float* momentum, void* weight,
+                         int32_t weight_dtype, float lr, float mu, int32_t nesterov, float weight_decay, float scale,
+                         void* workspace, size_t ws_bytes, void* stream) {
+  TraceRange trace("moe_muon_step");
+  MOE_TRY(check_ortho_config(cfg));
+  const moe_ortho_config& c = *cfg;
+  float abc[3 * kMaxOrthoSteps];
+  MOE_TRY(ortho_coeffs(c, coeffs, abc));
+  if (weight_dtype != MOE_DTYPE_F32 && weight_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  for (float v : {lr, mu, weight_decay, scale})
+    if (!isfinite(v)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_ortho_ws(c, workspace, ws_bytes));
+  if (c.n == 0) return MOE_OK;
+  MOE_TRY(need(g));
+  MOE_TRY(need(momentum));
+  MOE_TRY(need(weight));
+  OrthoParams p = {};
+  p.n = c.n; p.rows = c.rows; p.cols = c.cols; p.dtype = c.dtype; p.steps = c.steps;
+  p.eps = c.eps;
+  p.coeffs = abc;
+  p.g = g;
+  p.momentum = momentum;
+  p.mu = mu;
+  p.nesterov = nesterov != 0;
+  p.weight = weight;
+  p.weight_dtype = weight_dtype;
+  p.keep = (float)(1.0 - (double)lr * weight_decay);
+  p.step = (float)((double)lr * scale);
+  MOE_CUDA(launch_ortho(p, workspace, device_sm_count(), static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -276,6 +276,21 @@ cudaError_t launch_w4_quantize(int dtype, const void* w, long long n, int group,
 cudaError_t launch_w4_dequantize(int dtype, const void* q, const void* scale, const void* zero, long long n, int group,
                                  void* w, int num_sms, cudaStream_t s);
 
+// Newton-Schulz orthogonalisation and Muon's step (ortho_kernels.cu).
+struct OrthoParams {
+  int n, rows, cols, dtype, steps;
+  float eps;
+  const float* coeffs;      // host, [steps][3]
+  const void* g;
+  void* o;                  // bf16 result, or null: weight is updated
+  float* momentum;          // null: U = g
+  float mu; int nesterov;
+  void* weight; int weight_dtype;
+  float keep, step;         // weight = keep * weight - step * X
+};
+size_t ortho_workspace_bytes(int n_mat, int rows, int cols, int num_sms);
+cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cudaStream_t s);
+
 int device_sm_count();
 
 }  // namespace moe

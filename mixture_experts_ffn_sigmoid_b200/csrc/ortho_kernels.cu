@@ -1,0 +1,703 @@
+// Newton-Schulz orthogonalisation of a stack of matrices, bare or as the Muon
+// optimiser's update of momentum and weights: what follows the block's weight
+// gradients (expert stacks [E][f][d]) in training.
+//
+// For every matrix U of the stack (transposed first if it has more rows than
+// columns: m <= n below), with coefficients (a, b, c) per step:
+//
+//   X = U / (|U|_F + eps)
+//   repeat:  A = X X^T,  B = a I + b A + c A^2,  X = B X
+//
+// Each step applies p(s) = a s + b s^3 + c s^5 to the singular values, which
+// approach 1; the singular vectors stay. Muon: M = mu M + G, U = G + mu M
+// (Nesterov) or M, W = (1 - lr decay) W - lr scale X.
+//
+// What bounds it: the tensor cores. A step is 2 m^2 n + 2 m^3 + 2 m^2 n
+// operations; A and A^2 are symmetric, so the tiles above the diagonal are
+// not computed but written from those below: 3 m^2 n + m^3.
+//
+// Precision. The operands are fp16, accumulated in fp32 in TMEM, and rounded
+// once per product. X starts with norm 1 and its singular values stay in a
+// range that the host checks for the given coefficients, so fp16's range
+// suffices where bf16's is not needed and its three more bits count: five
+// steps end 1.2e-3 (2-norm) from fp64 for a spread spectrum, bf16 operands end
+// 1e-2 from it. X, A and B are stored times 64, so that small entries (1e-4
+// and below in wide matrices) stay above fp16's subnormals; powers of two cost
+// nothing. a I is folded into B: its rounding adds less than X's own.
+//
+// Kernels: one pass over U for its norm (and the momentum), one that writes X
+// in fp16 (transposing through shared memory), then three GEMM launches a step
+// of one persistent kernel on CTA pairs: 256 x 256 tiles by M = 256, N = 256
+// cta_group::2 MMAs, each CTA staging 128 rows of P and 128 of Q (32 KB per 64
+// of K, six stages), two accumulators in TMEM so that the epilogue of a tile
+// runs under the next one's MMAs. X is the MN-major operand of B X, so it is
+// stored once. The last step's epilogue writes the result or the weights.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "umma_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int NS_BK = 64;
+constexpr int NS_HALF = 128;                       // rows of a tile per CTA of the pair
+constexpr int NS_TILE = 2 * NS_HALF;
+constexpr int NS_OP_BYTES = NS_HALF * NS_BK * 2;   // one operand's share of a stage
+constexpr int NS_STAGE_BYTES = 2 * NS_OP_BYTES;
+constexpr int NS_STAGES = 6;
+constexpr int NS_EPI_WARPS = 8;
+constexpr int NS_THREADS = 32 * (2 + NS_EPI_WARPS);
+constexpr int NS_TMEM_COLS = 512;
+constexpr int NS_SMEM = 1024 + 1024 + NS_STAGES * NS_STAGE_BYTES;
+constexpr float kNsScale = 64.0f;                  // X, A and B are stored times this
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// TMA into this CTA's shared memory, completing on the pair leader's barrier.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (M = 256 over the pair) (+)= P Q^T, fp16 operands.
+__device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+enum NsMode { kNsGram = 0, kNsPoly = 1, kNsApply = 2, kNsLast = 3 };
+
+struct NsGemmParams {
+  int n_mat, m, n;          // X is [n_mat][m][n], m <= n
+  int ld_x, ld_a;           // row pitches (elements, multiples of 8) of X and of A, B
+  float a, b, c;            // kNsPoly
+  const __half* a_in;       // kNsPoly: A, read again in the epilogue
+  __half* out;              // kNsGram: A, kNsPoly: B, kNsApply: the next X
+  // kNsLast: the caller's matrices, [n_mat][rows][cols]; tall: out = X^T.
+  int tall, rows, cols;
+  __nv_bfloat16* o;         // result, or null:
+  void* weight;             // W = keep W - step X
+  int weight_f32;
+  float keep, step;
+  uint32_t* err;
+  long long timeout_ns;
+};
+
+struct NsTile {
+  int mat, i0, j0;          // first row and column of D
+};
+
+template <int MODE>
+__device__ __forceinline__ NsTile ns_tile(const NsGemmParams& p, int tile) {
+  const int tm = ceil_div(p.m, NS_TILE);
+  NsTile t;
+  if (MODE == kNsGram || MODE == kNsPoly) {      // tiles on and below the diagonal
+    const int per = tm * (tm + 1) / 2;
+    t.mat = tile / per;
+    const int r = tile - t.mat * per;
+    int i = (int)((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > r) --i;
+    while ((i + 1) * (i + 2) / 2 <= r) ++i;
+    t.i0 = i * NS_TILE;
+    t.j0 = (r - i * (i + 1) / 2) * NS_TILE;
+  } else {                                        // rows fastest: neighbours share X's columns
+    const int per = tm * ceil_div(p.n, NS_TILE);
+    t.mat = tile / per;
+    const int r = tile - t.mat * per;
+    t.j0 = (r / tm) * NS_TILE;
+    t.i0 = (r % tm) * NS_TILE;
+  }
+  return t;
+}
+
+__device__ __forceinline__ uint4 pack_half8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight columns of a row of the last product into the caller's matrices.
+__device__ __forceinline__ void ns_store_last(const NsGemmParams& p, int mat, int i, int j, const float (&v)[8]) {
+  const size_t base = (size_t)mat * p.rows * p.cols;
+  const bool vec = !p.tall && p.cols % 8 == 0;
+  const int nj = min(8, p.n - j);
+  if (p.o) {
+    if (vec) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(p.o + base + (size_t)i * p.cols + j) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < nj)
+          p.o[base + (p.tall ? (size_t)(j + e) * p.cols + i : (size_t)i * p.cols + j + e)] = __float2bfloat16_rn(v[e]);
+    }
+    return;
+  }
+  if (p.weight_f32) {
+    float* w = static_cast<float*>(p.weight) + base;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < nj) {
+        float& x = w[p.tall ? (size_t)(j + e) * p.cols + i : (size_t)i * p.cols + j + e];
+        x = p.keep * x - p.step * v[e];
+      }
+    return;
+  }
+  __nv_bfloat16* w = static_cast<__nv_bfloat16*>(p.weight) + base;
+  if (vec) {
+    uint4* at = reinterpret_cast<uint4*>(w + (size_t)i * p.cols + j);
+    const uint4 old = *at;
+    const uint32_t in[4] = {old.x, old.y, old.z, old.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lo = __uint_as_float(in[e] << 16), hi = __uint_as_float(in[e] & 0xffff0000u);
+      const __nv_bfloat162 h =
+          __floats2bfloat162_rn(p.keep * lo - p.step * v[2 * e], p.keep * hi - p.step * v[2 * e + 1]);
+      out[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *at = make_uint4(out[0], out[1], out[2], out[3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < nj) {
+      __nv_bfloat16& x = w[p.tall ? (size_t)(j + e) * p.cols + i : (size_t)i * p.cols + j + e];
+      x = __float2bfloat16_rn(p.keep * __bfloat162float(x) - p.step * v[e]);
+    }
+}
+
+// D = P Q^T (kNsGram: P = Q = X; kNsPoly: P = Q = A) or D = P Q with Q read
+// MN-major (kNsApply, kNsLast: P = B, Q = X).
+template <int MODE>
+__global__ void __launch_bounds__(NS_THREADS, 1)
+    ns_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                   const NsGemmParams p) {
+  constexpr bool SYM = MODE == kNsGram || MODE == kNsPoly;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty_bar = full_bar + NS_STAGES;
+  uint64_t* accf_bar = empty_bar + NS_STAGES;
+  uint64_t* acce_bar = accf_bar + 2;
+  uint64_t* drain_bar = acce_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  uint8_t* ring = smem + 1024;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS_STAGES; ++i) {
+      mbar_init(smem_u32(&full_bar[i]), 1);
+      mbar_init(smem_u32(&empty_bar[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&accf_bar[i]), 1);
+      mbar_init(smem_u32(&acce_bar[i]), 2 * NS_EPI_WARPS);
+    }
+    mbar_init(smem_u32(drain_bar), 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+    tmap_prefetch(&tmP);
+    tmap_prefetch(&tmQ);
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), NS_TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();             // both CTAs' barriers exist before either signals the other
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // What the launch before wrote is read only from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int tm = ceil_div(p.m, NS_TILE);
+  const int per = SYM ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, NS_TILE);
+  const int total = p.n_mat * per;
+  const int group = blockIdx.x >> 1, ngroups = gridDim.x >> 1;
+  const int nk = ceil_div(MODE == kNsGram ? p.n : p.m, NS_BK);
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ producer
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int tile = group; tile < total && ok; tile += ngroups) {
+      const NsTile t = ns_tile<MODE>(p, tile);
+      const int pi = t.i0 + (int)rank * NS_HALF, qj = t.j0 + (int)rank * NS_HALF;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.err, p.timeout_ns, true)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb_local = smem_u32(&full_bar[stage]);
+        const uint32_t fb = map_to_cta(fb_local, 0);
+        const uint32_t sp = smem_u32(ring + stage * NS_STAGE_BYTES), sq = sp + NS_OP_BYTES;
+        if (leader) mbar_expect_tx(fb_local, 2 * NS_STAGE_BYTES);   // both CTAs' copies
+        tma_load_3d_pair(sp, &tmP, kb * NS_BK, pi, t.mat, fb);
+        if (SYM) {
+          tma_load_3d_pair(sq, &tmQ, kb * NS_BK, qj, t.mat, fb);
+        } else {
+          tma_load_3d_pair(sq, &tmQ, qj, kb * NS_BK, t.mat, fb);
+          tma_load_3d_pair(sq + MN_BOX_BYTES, &tmQ, qj + 64, kb * NS_BK, t.mat, fb);
+        }
+        ++issued;
+        if (++stage == NS_STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (!ok && leader) {
+      // Giving up: the copies under way land before shared memory is freed.
+      const uint32_t n = issued < NS_STAGES ? issued : NS_STAGES;
+      for (uint32_t k = issued - n; k < issued; ++k)
+        wait_bounded(smem_u32(&full_bar[k % NS_STAGES]), (k / NS_STAGES) & 1u, abort_flag, p.err, p.timeout_ns, false);
+    }
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ------------------------------------------------------------ MMA issuer
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool issued = false, ok = true;
+    // fp16 x fp16 -> fp32, M = N = 256; bit 16: Q is MN-major.
+    const uint32_t idesc = (1u << 4) | ((uint32_t)(NS_TILE >> 3) << 17) | ((uint32_t)(NS_TILE >> 4) << 24) |
+                           (SYM ? 0u : 1u << 16);
+    for (int tile = group; tile < total && ok; tile += ngroups) {
+      if (!wait_bounded(smem_u32(&acce_bar[acc]), acc_phase ^ 1u, abort_flag, p.err, p.timeout_ns, true)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + (uint32_t)(acc * NS_TILE);
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!wait_bounded(smem_u32(&full_bar[stage]), phase, abort_flag, p.err, p.timeout_ns, true)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sp = smem_u32(ring + stage * NS_STAGE_BYTES);
+        const uint64_t pd = sw128_desc(sp);
+        const uint64_t qd = SYM ? sw128_desc(sp + NS_OP_BYTES) : sw128_mn_desc(sp + NS_OP_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < NS_BK / 16; ++kk) {
+          const uint64_t kp = (uint64_t)((kk * 32) >> 4);             // 16 k further along a row
+          const uint64_t kq = SYM ? kp : (uint64_t)((kk * 2 * 1024) >> 4);
+          umma_f16_pair(d, pd + kp, qd + kq, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+        }
+        issued = true;
+        umma_commit_pair(smem_u32(&empty_bar[stage]), 0x3);
+        if (++stage == NS_STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+      umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3);
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    if (issued) {                 // every MMA completes before TMEM is freed
+      umma_commit_pair(smem_u32(drain_bar), 0x1);
+      wait_bounded(smem_u32(drain_bar), 0u, abort_flag, p.err, p.timeout_ns, false);
+    }
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, cbeg = ((warp - 2) >> 2) * NS_HALF;   // TMEM lane quarter, column half
+    const uint32_t acce0 = map_to_cta(smem_u32(&acce_bar[0]), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = group; tile < total; tile += ngroups) {
+      const NsTile t = ns_tile<MODE>(p, tile);
+      const int i = t.i0 + (int)rank * NS_HALF + q * 32 + lane;
+      const int j0 = t.j0 + cbeg;
+      const int ncol = SYM ? p.m : p.n;
+      if (!wait_bounded(smem_u32(&accf_bar[acc]), acc_phase, abort_flag, p.err, p.timeout_ns, true)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * NS_TILE + cbeg);
+      for (int c0 = 0; c0 < NS_HALF && j0 + c0 < ncol; c0 += 32) {
+        uint32_t r[2][16];
+        tmem_ld16x2_wait(taddr + c0, taddr + c0 + 16, r[0], r[1]);
+        const int j = j0 + c0;
+        const bool row_ok = i < p.m;
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e >> 4][e & 15]);
+        if (MODE == kNsPoly) {
+          const __half* ap = p.a_in + ((size_t)t.mat * p.m + i) * p.ld_a + j;
+          uint4 av[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            av[k] = row_ok && j + 8 * k < ncol ? *reinterpret_cast<const uint4*>(ap + 8 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const __half2 h = reinterpret_cast<const __half2*>(av)[e >> 1];
+            float x = p.b * ((e & 1) ? __high2float(h) : __low2float(h)) + (p.c / kNsScale) * v[e];
+            if (j + e == i) x += p.a * kNsScale;
+            v[e] = x;
+          }
+        } else {
+          const float f = MODE == kNsLast ? 1.0f / (kNsScale * kNsScale) : 1.0f / kNsScale;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (!row_ok || j + 8 * k >= ncol) break;
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = v[8 * k + e];
+          if (MODE == kNsLast) {
+            ns_store_last(p, t.mat, i, j + 8 * k, w);
+          } else {   // a row's last eight may run into its padding
+            const int ld = SYM ? p.ld_a : p.ld_x;
+            *reinterpret_cast<uint4*>(p.out + ((size_t)t.mat * p.m + i) * ld + j + 8 * k) = pack_half8(w);
+          }
+        }
+        if (SYM && t.i0 != t.j0 && row_ok) {   // the tile above the diagonal: consecutive lanes, consecutive columns
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (j + e < ncol) p.out[((size_t)t.mat * p.m + j + e) * p.ld_a + i] = __float2half_rn(v[e]);
+        }
+        __syncwarp();             // the next TMEM load takes the whole warp
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acce0 + (uint32_t)acc * 8u);
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();             // the peer's shared memory and TMEM stay live until here
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, NS_TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------- norm and first X
+constexpr int NS_NORM_THREADS = 256;
+
+template <typename T> __device__ __forceinline__ void ns_load8(const T* p, float (&f)[8]);
+template <> __device__ __forceinline__ void ns_load8<float>(const float* p, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+template <> __device__ __forceinline__ void ns_load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// Sum of squares of U per matrix and block (fp32), with the momentum updated
+// on the way. A matrix is one run of size = rows * cols elements; `vec` where
+// every eight of them are aligned. Block (0, 0) clears the error word.
+template <typename T, bool MOM>
+__global__ void __launch_bounds__(NS_NORM_THREADS) ns_norm_kernel(const T* __restrict__ g, float* __restrict__ mom,
+                                                                  float mu, int nesterov, long long size, int vec,
+                                                                  float* __restrict__ partial, uint32_t* err) {
+  __shared__ float red[NS_NORM_THREADS / 32];
+  if (err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *err = 0u;
+  const size_t base = (size_t)blockIdx.y * size;
+  const long long step = (long long)gridDim.x * NS_NORM_THREADS;
+  float s = 0.0f;
+  auto one = [&](float gv, float* mp) {
+    float u = gv;
+    if (MOM) {
+      const float m = fmaf(mu, *mp, gv);
+      *mp = m;
+      u = nesterov ? fmaf(mu, m, gv) : m;
+    }
+    s = fmaf(u, u, s);
+  };
+  if (vec) {
+    for (long long i = ((long long)blockIdx.x * NS_NORM_THREADS + threadIdx.x); i < size / 8; i += step) {
+      float f[8], m[8];
+      ns_load8(g + base + i * 8, f);
+      if (MOM) ns_load8(mom + base + i * 8, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) one(f[e], &m[e]);
+      if (MOM) {
+        float4* mp = reinterpret_cast<float4*>(mom + base + i * 8);
+        mp[0] = make_float4(m[0], m[1], m[2], m[3]);
+        mp[1] = make_float4(m[4], m[5], m[6], m[7]);
+      }
+    }
+  } else {
+    for (long long i = (long long)blockIdx.x * NS_NORM_THREADS + threadIdx.x; i < size; i += step) {
+      float m = MOM ? mom[base + i] : 0.0f;
+      one(to_f32(g[base + i]), &m);
+      if (MOM) mom[base + i] = m;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0f;
+    for (int w = 0; w < NS_NORM_THREADS / 32; ++w) s += red[w];
+    partial[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+  }
+}
+
+// X = 64 U / (|U| + eps) in fp16, [m][ld]; a block takes 64 x 64 elements of U.
+template <typename T, bool MOM>
+__global__ void __launch_bounds__(256) ns_init_kernel(const T* __restrict__ g, const float* __restrict__ mom, float mu,
+                                                      int nesterov, int rows, int cols, int vec, int tall, float eps,
+                                                      const float* __restrict__ partial, int n_partial, int col_tiles,
+                                                      __half* __restrict__ x, int ld) {
+  __shared__ float red[8];
+  __shared__ __half tile[64][72];
+  const int tid = threadIdx.x, mat = blockIdx.y;
+  float s = 0.0f;
+  for (int i = tid; i < n_partial; i += 256) s += partial[(size_t)mat * n_partial + i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((tid & 31) == 0) red[tid >> 5] = s;
+  __syncthreads();
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) s += red[w];
+  const float scale = kNsScale / (sqrtf(s) + eps);
+  const int r0 = (blockIdx.x / col_tiles) * 64, c0 = (blockIdx.x % col_tiles) * 64;
+  const size_t base = (size_t)mat * rows * cols;
+  __half* xm = x + (size_t)mat * (tall ? cols : rows) * ld;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = r0 + k * 32 + tid / 8, c = c0 + (tid % 8) * 8;
+    float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (r < rows && c < cols) {
+      const size_t at = base + (size_t)r * cols + c;
+      if (vec) {
+        if (!MOM || nesterov) ns_load8(g + at, f);
+        if (MOM) {
+          float m[8];
+          ns_load8(mom + at, m);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = nesterov ? fmaf(mu, m[e], f[e]) : m[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < cols) {
+            f[e] = to_f32(g[at + e]);
+            if (MOM) f[e] = nesterov ? fmaf(mu, mom[at + e], f[e]) : mom[at + e];
+          }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= scale;
+    const uint4 h = pack_half8(f);
+    if (!tall) {
+      if (r < rows && c < cols) *reinterpret_cast<uint4*>(xm + (size_t)r * ld + c) = h;
+    } else {
+      *reinterpret_cast<uint4*>(&tile[k * 32 + tid / 8][(tid % 8) * 8]) = h;
+    }
+  }
+  if (!tall) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int c = k * 32 + tid / 8, r = (tid % 8) * 8;    // row c of X, eight of its columns
+    if (c0 + c >= cols || r0 + r >= rows) continue;
+    __align__(16) __half h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = tile[r + e][c];
+    *reinterpret_cast<uint4*>(xm + (size_t)(c0 + c) * ld + r0 + r) = *reinterpret_cast<const uint4*>(h);
+  }
+}
+
+// fp16 [outer][rows][cols] with a row pitch, 128-byte swizzle, box 64 x box_rows.
+bool make_ns_tmap(CUtensorMap* tm, const void* base, long long cols, long long rows, long long outer, long long ld,
+                  int box_rows) {
+  auto fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
+  cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(rows * ld * 2)};
+  cuuint32_t box[3] = {(cuuint32_t)NS_BK, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t launch_ns_gemm(const CUtensorMap& tp, const CUtensorMap& tq, const NsGemmParams& p, int num_sms,
+                           cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};   // devices whose limit is raised, one bit each
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((done.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(ns_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+  }
+  const long long tm = ceil_div(p.m, NS_TILE);
+  const long long tiles = p.n_mat * (MODE == kNsGram || MODE == kNsPoly ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, NS_TILE));
+  const int pairs = num_sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
+  cfg.blockDim = dim3(NS_THREADS);
+  cfg.dynamicSmemBytes = NS_SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, ns_gemm_kernel<MODE>, tp, tq, p);
+}
+
+constexpr size_t kNsAlign = 256;
+size_t ns_round(size_t v) { return (v + kNsAlign - 1) / kNsAlign * kNsAlign; }
+
+struct NsPlan {
+  int m, n, ld_x, ld_a;
+  int batch;                // matrices worked on at once
+  int norm_blocks;          // partial sums per matrix
+  size_t err, partial, x0, x1, a, b, total;
+};
+
+// A matrix is independent of the others; enough of them run together to give
+// the smallest product (tiles of A) about eight rounds of tiles per CTA pair,
+// and no more, so that the scratch stays small and near L2's size.
+NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
+  NsPlan q;
+  q.m = rows < cols ? rows : cols;
+  q.n = rows < cols ? cols : rows;
+  q.ld_x = (q.n + 7) / 8 * 8;
+  q.ld_a = (q.m + 7) / 8 * 8;
+  const long long t = ceil_div(q.m, NS_TILE), tiles = t * (t + 1) / 2;
+  long long most = ceil_div_ll(8LL * (num_sms / 2), tiles);
+  if (most > 32768) most = 32768;
+  const long long rounds = ceil_div_ll(n_mat > 0 ? n_mat : 1, most);
+  q.batch = (int)ceil_div_ll(n_mat > 0 ? n_mat : 1, rounds);
+  const long long size = (long long)rows * cols, blocks = ceil_div_ll(size, NS_NORM_THREADS * 8 * 4);
+  q.norm_blocks = (int)(blocks < 256 ? blocks : 256);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += ns_round(bytes);
+    return o;
+  };
+  q.err = take(kNsAlign);
+  q.partial = take((size_t)q.batch * q.norm_blocks * 4);
+  q.x0 = take((size_t)q.batch * q.m * q.ld_x * 2);
+  q.x1 = take((size_t)q.batch * q.m * q.ld_x * 2);
+  q.a = take((size_t)q.batch * q.m * q.ld_a * 2);
+  q.b = take((size_t)q.batch * q.m * q.ld_a * 2);
+  q.total = off;
+  return q;
+}
+
+template <typename T, bool MOM>
+cudaError_t ns_first_x(const OrthoParams& p, const NsPlan& q, int first, int count, char* ws, bool clear,
+                       cudaStream_t s) {
+  const long long size = (long long)p.rows * p.cols;
+  const T* g = static_cast<const T*>(p.g) + (size_t)first * size;
+  float* mom = MOM ? p.momentum + (size_t)first * size : nullptr;
+  float* partial = reinterpret_cast<float*>(ws + q.partial);
+  ns_norm_kernel<T, MOM><<<dim3(q.norm_blocks, count), NS_NORM_THREADS, 0, s>>>(
+      g, mom, p.mu, p.nesterov, size, size % 8 == 0, partial, clear ? reinterpret_cast<uint32_t*>(ws + q.err) : nullptr);
+  const int col_tiles = ceil_div(p.cols, 64);
+  ns_init_kernel<T, MOM><<<dim3((unsigned)(col_tiles * (long long)ceil_div(p.rows, 64)), count), 256, 0, s>>>(
+      g, mom, p.mu, p.nesterov, p.rows, p.cols, p.cols % 8 == 0, p.rows > p.cols, p.eps, partial, q.norm_blocks,
+      col_tiles, reinterpret_cast<__half*>(ws + q.x0), q.ld_x);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t ortho_workspace_bytes(int n_mat, int rows, int cols, int num_sms) {
+  return ns_plan(n_mat, rows, cols, num_sms).total;
+}
+
+cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cudaStream_t s) {
+  const NsPlan q = ns_plan(p.n, p.rows, p.cols, num_sms);
+  char* ws = static_cast<char*>(workspace);
+  __half* x[2] = {reinterpret_cast<__half*>(ws + q.x0), reinterpret_cast<__half*>(ws + q.x1)};
+  __half *a = reinterpret_cast<__half*>(ws + q.a), *b = reinterpret_cast<__half*>(ws + q.b);
+  CUtensorMap xk[2], xn[2], ak, bk;
+  for (int i = 0; i < 2; ++i)
+    if (!make_ns_tmap(&xk[i], x[i], q.n, q.m, q.batch, q.ld_x, NS_HALF) ||
+        !make_ns_tmap(&xn[i], x[i], q.n, q.m, q.batch, q.ld_x, NS_BK))
+      return cudaErrorInvalidValue;
+  if (!make_ns_tmap(&ak, a, q.m, q.m, q.batch, q.ld_a, NS_HALF) ||
+      !make_ns_tmap(&bk, b, q.m, q.m, q.batch, q.ld_a, NS_HALF))
+    return cudaErrorInvalidValue;
+  const size_t size = (size_t)p.rows * p.cols;
+  for (int first = 0; first < p.n; first += q.batch) {
+    const int count = p.n - first < q.batch ? p.n - first : q.batch;
+    const bool f32 = p.dtype == MOE_DTYPE_F32, mom = p.momentum != nullptr;
+    cudaError_t e =
+        f32 ? (mom ? ns_first_x<float, true>(p, q, first, count, ws, first == 0, s)
+                   : ns_first_x<float, false>(p, q, first, count, ws, first == 0, s))
+            : (mom ? ns_first_x<__nv_bfloat16, true>(p, q, first, count, ws, first == 0, s)
+                   : ns_first_x<__nv_bfloat16, false>(p, q, first, count, ws, first == 0, s));
+    if (e != cudaSuccess) return e;
+    NsGemmParams g = {};
+    g.n_mat = count;
+    g.m = q.m; g.n = q.n;
+    g.ld_x = q.ld_x; g.ld_a = q.ld_a;
+    g.a_in = a;
+    g.tall = p.rows > p.cols;
+    g.rows = p.rows; g.cols = p.cols;
+    g.o = p.o ? static_cast<__nv_bfloat16*>(p.o) + first * size : nullptr;
+    g.weight_f32 = p.weight_dtype == MOE_DTYPE_F32;
+    g.weight = p.weight ? static_cast<char*>(p.weight) + first * size * (g.weight_f32 ? 4 : 2) : nullptr;
+    g.keep = p.keep;
+    g.step = p.step;
+    g.err = reinterpret_cast<uint32_t*>(ws + q.err);
+    g.timeout_ns = kDefaultTimeoutNs;
+    for (int k = 0; k < p.steps; ++k) {
+      const int cur = k & 1;
+      g.a = p.coeffs[3 * k]; g.b = p.coeffs[3 * k + 1]; g.c = p.coeffs[3 * k + 2];
+      g.out = a;
+      if ((e = launch_ns_gemm<kNsGram>(xk[cur], xk[cur], g, num_sms, s)) != cudaSuccess) return e;
+      g.out = b;
+      if ((e = launch_ns_gemm<kNsPoly>(ak, ak, g, num_sms, s)) != cudaSuccess) return e;
+      g.out = x[cur ^ 1];
+      e = k + 1 < p.steps ? launch_ns_gemm<kNsApply>(bk, xn[cur], g, num_sms, s)
+                          : launch_ns_gemm<kNsLast>(bk, xn[cur], g, num_sms, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace moe

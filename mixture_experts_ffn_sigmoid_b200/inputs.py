@@ -101,6 +101,18 @@ class NormConfig:
         return -(-self.T // self.gate_tokens)
 
 
+@dataclasses.dataclass(frozen=True)
+class OrthoConfig:
+    """A stack of n matrices [rows, cols] to orthogonalise by Newton-Schulz
+    products (``dtype``: of the gradients)."""
+    n: int
+    rows: int
+    cols: int
+    dtype: str = "bf16"            # "bf16" or "f32"
+    steps: int = 5
+    eps: float = 1e-7
+
+
 CONFIGS = {
     "tiny_fp32": MoEConfig("tiny_fp32", T=64, d=128, E=8, k=2, f=256, dtype="f32"),
     "mixtral_8x7b": MoEConfig("mixtral_8x7b", T=4096, d=4096, E=8, k=2, f=14336),

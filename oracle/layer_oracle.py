@@ -83,3 +83,33 @@ def swiglu_rows(x, w1, w3, w2):
     a, b = x @ w1.T, x @ w3.T
     h = a / (1.0 + np.exp(-a)) * b
     return h @ w2.T, a, b, h
+
+
+# --------------------------------------------------------- orthogonalisation
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def newton_schulz(u, coeffs, eps=1e-7, stored=lambda v: v):
+    """X of the Newton-Schulz steps for one matrix u; coeffs [(a, b, c)] per
+    step. ``stored`` rounds what an implementation keeps between products (X,
+    A = X X^T and a I + b A + c A^2): the identity gives the exact result."""
+    if u.shape[0] > u.shape[1]:
+        return newton_schulz(u.T, coeffs, eps, stored).T
+    x = stored(u / (np.sqrt((u * u).sum()) + eps))
+    for k, (a, b, c) in enumerate(coeffs):
+        g = stored(x @ x.T)
+        x = stored(a * np.eye(len(g)) + b * g + c * (g @ g)) @ x
+        if k + 1 < len(coeffs):
+            x = stored(x)
+    return x
+
+
+def half_64(v):
+    """v rounded to IEEE half precision at 64 times its size."""
+    return (v * 64.0).astype(np.float16).astype(np.float64) / 64.0
+
+
+def muon_direction(g, momentum, mu, nesterov):
+    """(new momentum, U)."""
+    m = mu * momentum + g
+    return m, g + mu * m if nesterov else m

@@ -45,3 +45,23 @@ def test_residual_norm_backward_against_differences(post, gate, pre, offset):
         # A central difference is off by e^2 times a third derivative of order
         # one, and by rounding of order 1e-15 / e.
         assert abs(diff - want) <= 1e-7 * max(1.0, abs(want)), name
+
+
+def test_newton_schulz_acts_on_singular_values():
+    rng = np.random.default_rng(0)
+    for shape in ((4, 7), (7, 4), (5, 5)):
+        u = rng.standard_normal(shape)
+        left, s, right = np.linalg.svd(u, full_matrices=False)
+        s = s / (np.sqrt((s * s).sum()) + 1e-7)
+        coeffs = [lo.MUON_COEFFS, (1.5, -0.5, 0.0), (2.0, -1.5, 0.5)]
+        for a, b, c in coeffs:
+            s = a * s + b * s ** 3 + c * s ** 5
+        assert np.allclose(lo.newton_schulz(u, coeffs), (left * s) @ right, rtol=0, atol=1e-13)
+
+
+def test_swiglu_rows_and_w4_dense_by_hand():
+    q, scale = np.array([[0x98, 0x07]], dtype=np.uint8), np.array([[0.5, 2.0]])
+    assert np.array_equal(lo.w4_dense(q, scale, None, 2), [[0.0, 0.5, -2.0, -16.0]])
+    assert np.array_equal(lo.w4_dense(q, scale, np.array([[8, 7]], dtype=np.uint8), 2), [[0.0, 0.5, 0.0, -14.0]])
+    y, a, b, h = lo.swiglu_rows(np.array([[1.0]]), np.array([[2.0]]), np.array([[3.0]]), np.array([[4.0]]))
+    assert np.allclose(y, 4 * 3 * 2 / (1 + np.exp(-2.0)))

@@ -216,3 +216,76 @@ def test_w4_block_binding():
             B.moe_forward_w4(cfg, **{**a, name: bad})
     with pytest.raises(TypeError, match="w1"):
         B.moe_forward_w4(cfg, **{**a, "w1": torch.zeros(4, 64, 128)})
+
+
+# --------------------------------------------------------- orthogonalisation
+def ortho(**kw):
+    return B.make_ortho_config(**{**dict(n=2, rows=64, cols=96), **kw})
+
+
+def call_ortho(c, coeffs=None, g=FAKE, o=FAKE, ws=FAKE, n=BIG):
+    return B.lib().moe_orthogonalize(ctypes.byref(c) if c else None, coeffs, g, o, ws, n, None)
+
+
+def call_muon(c, coeffs=None, g=FAKE, m=FAKE, w=FAKE, wd=0, lr=0.1, mu=0.9, decay=0.0, scale=1.0, ws=FAKE, n=BIG):
+    return B.lib().moe_muon_step(ctypes.byref(c) if c else None, coeffs, g, m, w, wd, lr, mu, 1, decay, scale, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), B.MOE_ERR_INVALID_ARG), (dict(rows=0), B.MOE_ERR_INVALID_ARG), (dict(cols=-4), B.MOE_ERR_INVALID_ARG),
+    (dict(steps=0), B.MOE_ERR_INVALID_ARG), (dict(steps=65), B.MOE_ERR_INVALID_ARG), (dict(eps=0.0), B.MOE_ERR_INVALID_ARG),
+    (dict(eps=float("inf")), B.MOE_ERR_INVALID_ARG), (dict(rows=65537), B.MOE_ERR_UNSUPPORTED),
+    (dict(cols=65537), B.MOE_ERR_UNSUPPORTED)])
+def test_ortho_settings(kw, status):
+    c = ortho(**kw)
+    assert B.ortho_workspace_size(c) == 0
+    assert call_ortho(c) == status and call_muon(c) == status
+
+
+def test_ortho_pointers_and_workspace():
+    c, bad, odd = ortho(), B.MOE_ERR_INVALID_ARG, B.MOE_ERR_MISALIGNED
+    assert call_ortho(None) == bad and call_muon(None) == bad
+    for kw in (dict(g=None), dict(o=None), dict(ws=None)):
+        assert call_ortho(c, **kw) == bad
+    for kw in (dict(g=ODD), dict(o=ODD), dict(ws=ODD)):
+        assert call_ortho(c, **kw) == odd
+    for kw in (dict(g=None), dict(m=None), dict(w=None), dict(ws=None), dict(wd=2), dict(lr=float("nan")),
+               dict(mu=float("inf")), dict(decay=float("nan")), dict(scale=float("inf"))):
+        assert call_muon(c, **kw) == bad
+    for kw in (dict(g=ODD), dict(m=ODD), dict(w=ODD)):
+        assert call_muon(c, **kw) == odd
+    need = B.ortho_workspace_size(c)
+    assert need > 0 and call_ortho(c, n=need - 1) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert call_muon(c, n=need - 1) == B.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert call_ortho(ortho(n=0), g=None, o=None) == B.MOE_OK
+
+
+@pytest.mark.parametrize("abc,ok", [
+    ((1.5, -0.5, 0.0), True), ((2.0, -1.5, 0.5), True), ((float("nan"), 0.0, 0.0), False),
+    ((3.0, 0.0, 0.0), False),          # 3^5 of the largest singular value
+    ((1.0, 600.0, -600.0), False)])
+def test_coefficients_that_leave_the_range_are_refused(abc, ok):
+    c = ortho()
+    arr = (ctypes.c_float * 15)(*abc * 5)
+    # A good set gets as far as the missing gradients.
+    assert call_ortho(c, arr, g=None if ok else FAKE) == B.MOE_ERR_INVALID_ARG
+    if ok:
+        assert call_ortho(c, arr, g=ODD) == B.MOE_ERR_MISALIGNED
+
+
+def test_ortho_binding():
+    z = lambda dt=bf: torch.zeros(2, 64, 96, dtype=dt)
+    from mixture_experts_ffn_sigmoid_b200.inputs import OrthoConfig
+    c, ws = OrthoConfig(n=2, rows=64, cols=96), torch.zeros(8, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.moe_orthogonalize(c, z(), z(), ws)
+    with pytest.raises(ValueError, match="g"):
+        B.moe_orthogonalize(c, z(torch.float32), z(), ws)
+    with pytest.raises(ValueError, match="o"):
+        B.moe_orthogonalize(c, z(), z()[:1], ws)
+    with pytest.raises(ValueError, match="coeffs"):
+        B.moe_orthogonalize(c, z(), z(), ws, coeffs=[(1.0, 2.0, 3.0)] * 2)
+    with pytest.raises(ValueError, match="momentum"):
+        B.moe_muon_step(c, z(), z(), z(), ws, lr=0.1)
+    with pytest.raises(ValueError, match="weight"):
+        B.moe_muon_step(c, z(), z(torch.float32), z(torch.float16), ws, lr=0.1)
