@@ -513,8 +513,8 @@ typedef struct {
  *
  *   w       [rows][K]  dtype  16-byte aligned
  *   out     q, scale and zero receive the result; zero = NULL centres the codes
- *           on 8 with scale = bf16(max|w| / 7) per group, else scale =
- *           bf16((max(w, 0) - min(w, 0)) / 15) and zero = round(-min(w, 0) / scale)
+ *           on 8 with scale = bf16(max|w| * fp32(1/7)) per group, else scale =
+ *           bf16((max(w, 0) - min(w, 0)) * fp32(1/15)), zero = round(-min(w, 0) / scale)
  *
  * code = round(w / scale) + zero, clamped to 0..15, ties to even, all in fp32.
  * A group of zeros has scale 0; a group with an infinity or NaN has scale NaN.

@@ -16,20 +16,28 @@
 // shared memory first, four times the bytes that HBM delivers.
 //
 // Unpacking: a 32-bit word holds eight codes c0..c7 of consecutive k. (w >> 4i)
-// & 0x000f000f is the pair (ci, c(i+4)); OR-ed with 0x4300 it is bf16 128 +
-// code, from which 128 + zero is subtracted exactly. The products therefore
-// run over exact small integers; the scale is applied in fp32 to each group's
-// accumulator, so no weight is ever rounded. The order of k inside a group is
+// & 0x000f000f is the pair (ci, c(i+4)); OR-ed with 0x4300 it is the pair of
+// bf16 numbers 128 + code. The products run over these, and the 128 + zero
+// that is too much comes off each group's sum in fp32, sum_k x_k of the group
+// being one more product with a matrix of ones (shared by every row): seven
+// integer instructions per eight weights and no arithmetic on them. The group's
+// fp32 sum then takes its scale. No weight is rounded; the sums run about 30
+// times as large as the result, which costs five of fp32's 24 bits and stays
+// far below the rounding of the bf16 output. The order of k inside a group is
 // free as long as both operands agree: token rows are paired the same way
-// (x_i, x_(i+4)).
+// (x_i, x_(i+4)), by byte permutes in gate/up; h is written in that order, so
+// the down product needs none.
 //
 // Layout of the work: a CTA of 8 warps takes a contiguous run of units; a unit
-// is 16 WM weight rows of one expert (times up to 8 NT of its token rows), its
-// K split over WK = 8 / WM warps in chunks of 128. Each warp streams its chunks
-// through a ring of cp.async stages of its own, across unit boundaries, so
-// weights keep flowing while a unit's partial sums meet in shared memory. Units
-// of the non-empty segments only are dealt, evenly, so a batch that touches
-// few experts still uses every SM.
+// is 16 WM rows of W1 and W3 (32 WM rows of W2) of one expert times up to 8 NT
+// of its token rows, its K split over WK = 8 / WM warps in chunks of 128, two
+// 16-row tiles a warp, which share the token fragments. Each warp streams its
+// chunks through a ring of cp.async stages of its own, across unit boundaries,
+// so weights keep flowing while a unit's partial sums meet in shared memory.
+// Units of the non-empty segments only are dealt, evenly, so a batch that
+// touches few experts still uses every SM.
+#include <type_traits>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -56,15 +64,10 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The four bf16 pairs (ci - z, c(i+4) - z), z128 = 128 + zero in both halves.
-__device__ __forceinline__ void unpack_w4(uint32_t w, uint32_t z128, uint32_t (&p)[4]) {
+// The four bf16 pairs (128 + ci, 128 + c(i+4)) of a word.
+__device__ __forceinline__ void unpack_w4(uint32_t w, uint32_t (&p)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&z128));
-    p[i] = *reinterpret_cast<const uint32_t*>(&d);
-  }
+  for (int i = 0; i < 4; ++i) p[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
 }
 
 struct W4Seg {   // one segment's share of a unit
@@ -79,11 +82,15 @@ struct W4Seg {   // one segment's share of a unit
 // its expert (n_routed: the dense one), z = its first token row, w = its rows.
 using W4Entry = int4;
 
-template <int MATS, int NT>
+// MATS = 2: gate/up, the two tiles of a warp are the same rows of W1 and W3.
+// MATS = 1: down, they are 16 rows of W2 and the 16 after them. SUBN: groups
+// in a chunk of 128.
+template <int MATS, int NT, int SUBN>
 __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmParams p, int WK) {
   constexpr int W4_STAGES = w4_stages<NT>();
-  constexpr int STAGE = MATS * W4_MAT_BYTES + W4_SC_BYTES;
-  constexpr int RED = MATS * NT * 32;                     // float4s of one warp's partial sums
+  constexpr int STAGE = 2 * W4_MAT_BYTES + W4_SC_BYTES;
+  constexpr int RED = 2 * NT * 32;                        // float4s of one warp's partial sums
+  constexpr int WROWS = MATS == 2 ? 16 : 32;              // weight rows of a warp
   extern __shared__ __align__(128) uint8_t w4_dyn[];
   __shared__ int warp_n[W4_WARPS];
   __shared__ long long warp_u[W4_WARPS];
@@ -95,7 +102,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
 
   // -------------------------------------------------- the segments' table
   const int n_seg = p.n_routed + (p.dense_rows > 0 ? 1 : 0);
-  const int unit_rows = 16 * WM;
+  const int unit_rows = WROWS * WM;
   int base_n = 0;
   long long base_u = 0;
   for (int s0 = 0; s0 < n_seg; s0 += W4_THREADS) {
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
     const int pass = rel % passes;
     sg.t0 = begin + pass * 8 * NT;
     sg.rows = min(8 * NT, rows - pass * 8 * NT);
-    m0 = (rel / passes) * unit_rows + wm * 16;
+    m0 = (rel / passes) * unit_rows + wm * WROWS;
   };
   // The first segment by halving: later ones follow one by one.
   int first_seg = 0;
@@ -176,54 +183,74 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
   }
 
   // ------------------------------------------------------- weight stream
-  const int sub_n = W4_CHUNK / p.group;             // groups of a chunk: 1, 2 or 4
-  int pu = u0, phint = first_seg, pm0 = 0, pc = wk;
-  W4Seg ps = {};
-  if (pu < u1) locate(pu, phint, ps, pm0);
-  uint16_t sc_r[MATS][2];
-  uint8_t z_r[MATS][2];
+  int pu = u0, phint = first_seg, pc = 0, pn = 0, pK = 0, pgroups = 0;   // the next chunk: unit, index, count
+  const uint8_t* pq[2] = {nullptr, nullptr};         // this lane's 16 codes bytes of row g, per tile
+  const uint16_t* psc[2] = {nullptr, nullptr};       // row g's scales
+  const uint8_t* pz[2] = {nullptr, nullptr};         // and zero points, or null
+  bool p_ok[2] = {false, false};                     // the tile lies inside the matrix (M is a multiple of 32)
+  uint16_t sc_r[2][2];
+  uint8_t z_r[2][2];
   int sc_slot = -1;                                  // stage that the loaded scales belong to
 #pragma unroll
-  for (int a = 0; a < MATS; ++a) sc_r[a][0] = sc_r[a][1] = z_r[a][0] = z_r[a][1] = 0;
+  for (int a = 0; a < 2; ++a) sc_r[a][0] = sc_r[a][1] = z_r[a][0] = z_r[a][1] = 0;
 
+  auto open_unit = [&]() {                           // pointers of unit pu
+    W4Seg sg;
+    int m0;
+    locate(pu, phint, sg, m0);
+    pK = sg.K;
+    pn = ceil_div(sg.K, W4_CHUNK);
+    pgroups = sg.K / p.group;
+    pc = wk;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const W4Operand& op = sg.op[MATS == 2 ? a : 0];
+      const int m = MATS == 2 ? m0 : m0 + 16 * a;
+      p_ok[a] = m < sg.M;
+      const size_t row = sg.row0 + (p_ok[a] ? m + g : 0);
+      pq[a] = op.q + row * (size_t)(sg.K / 2) + q * 16;
+      psc[a] = static_cast<const uint16_t*>(op.scale) + row * pgroups;
+      pz[a] = op.zero ? op.zero + row * pgroups : nullptr;
+    }
+  };
   auto store_scales = [&]() {
     if (sc_slot < 0) return;
-    uint32_t v[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int a = 0; a < MATS; ++a) {
-      v[a] = (uint32_t)sc_r[a][0] | ((uint32_t)sc_r[a][1] << 16);
-      v[2 + a] = (uint32_t)z_r[a][0] | ((uint32_t)z_r[a][1] << 16);
-    }
-    *reinterpret_cast<uint4*>(ring + (size_t)sc_slot * STAGE + MATS * W4_MAT_BYTES + lane * 16) =
-        make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(ring + (size_t)sc_slot * STAGE + 2 * W4_MAT_BYTES + lane * 16) =
+        make_uint4((uint32_t)sc_r[0][0] | ((uint32_t)sc_r[0][1] << 16), (uint32_t)sc_r[1][0] | ((uint32_t)sc_r[1][1] << 16),
+                   (uint32_t)z_r[0][0] | ((uint32_t)z_r[0][1] << 16), (uint32_t)z_r[1][0] | ((uint32_t)z_r[1][1] << 16));
     sc_slot = -1;
   };
+  // Where this lane's pieces of a tile go in a stage: 64 bytes a row, its
+  // 16-byte pieces swapped about so that the word reads below and these
+  // writes each take every bank once.
+  const uint32_t ring_s = w4_smem(ring), put = g * 64 + ((q ^ ((g >> 1) & 3)) * 16);
   // Start the next chunk of this warp's stream into stage `slot`. Its scales
   // come by plain loads and are put into the stage at the next call, when
   // they have arrived.
   auto issue = [&](int slot) {
     store_scales();
-    while (pu < u1 && pc >= ceil_div(ps.K, W4_CHUNK)) {
-      if (++pu < u1) locate(pu, phint, ps, pm0);
-      pc = wk;
+    while (pu < u1 && pc >= pn) {
+      if (++pu < u1) open_unit();
     }
     if (pu < u1) {
-      const int k0 = pc * W4_CHUNK, groups = ps.K / p.group;
-      const uint32_t dst = w4_smem(ring + (size_t)slot * STAGE);
-      const int gi = min(k0 / p.group + (q & (sub_n - 1)), groups - 1);
+      const uint32_t dst = ring_s + slot * STAGE + put;
+      const bool in_k = pc * W4_CHUNK + q * 32 < pK;
+      const int gi = min(pc * SUBN + (q & (SUBN - 1)), pgroups - 1);
+      const size_t row8 = (size_t)pK * 4;            // eight rows of codes
 #pragma unroll
-      for (int a = 0; a < MATS; ++a) {
-        const W4Operand& op = ps.op[a];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = g + 8 * h;
-          const bool row_ok = pm0 + r < ps.M;
-          const size_t row = ps.row0 + (row_ok ? pm0 + r : 0);
-          const bool ok = row_ok && k0 + q * 32 < ps.K;
-          cp_async16_zfill(dst + a * W4_MAT_BYTES + r * 64 + ((q ^ ((r >> 1) & 3)) * 16),
-                           op.q + row * (size_t)(ps.K / 2) + (ok ? (k0 + q * 32) / 2 : 0), ok);
-          sc_r[a][h] = __ldg(static_cast<const uint16_t*>(op.scale) + row * groups + gi);
-          z_r[a][h] = op.zero ? __ldg(op.zero + row * groups + gi) : (uint8_t)8;
+      for (int a = 0; a < 2; ++a) {
+        const bool ok = p_ok[a] && in_k;
+        const uint8_t* src = ok ? pq[a] + pc * (W4_CHUNK / 2) : pq[a] - q * 16;
+        cp_async16_zfill(dst + a * W4_MAT_BYTES, src, ok);
+        cp_async16_zfill(dst + a * W4_MAT_BYTES + 512, ok ? src + row8 : src, ok);
+        const int g8 = p_ok[a] ? 8 * pgroups : 0;
+        sc_r[a][0] = __ldg(psc[a] + gi);
+        sc_r[a][1] = __ldg(psc[a] + gi + g8);
+        if (pz[a]) {
+          z_r[a][0] = __ldg(pz[a] + gi);
+          z_r[a][1] = __ldg(pz[a] + gi + g8);
+        } else {
+          z_r[a][0] = z_r[a][1] = 8;
         }
       }
       sc_slot = slot;
@@ -231,10 +258,15 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  if (pu < u1) open_unit();
   for (int i = 0; i < W4_STAGES - 1; ++i) issue(i);
   if (p.wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ------------------------------------------------------------- products
+  const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+  uint32_t get[4];                                   // word s * 4 + q of row g in a stage
+#pragma unroll
+  for (int s = 0; s < 4; ++s) get[s] = g * 64 + ((s ^ ((g >> 1) & 3)) * 16) + q * 4;
   int slot = 0, hint = first_seg;
   for (int u = u0; u < u1; ++u) {
     W4Seg sg;
@@ -252,12 +284,12 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
           src = v >= 0 && v < p.gather_rows ? v : 0;
         }
         xrow[t] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s : p.x) +
-                                                 src * (size_t)sg.K);
+                                                 src * (size_t)sg.K) + q;
       }
     }
-    float acc[MATS][NT][4];
+    float acc[2][NT][4];
 #pragma unroll
-    for (int a = 0; a < MATS; ++a)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -265,52 +297,67 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
     const int nch = ceil_div(sg.K, W4_CHUNK);
     for (int c = wk; c < nch; c += WK) {
       issue(slot == 0 ? W4_STAGES - 1 : slot - 1);
+      auto load_x = [&](int t, int s) -> uint4 {     // eight k of a token row
+        const int k32 = c * 4 + s;
+        return xrow[t] && k32 * 32 < sg.K ? *(xrow[t] + k32 * 4) : make_uint4(0, 0, 0, 0);
+      };
+      uint4 xv[NT == 1 ? 4 : 1];                     // with one token tile: fetched before the wait
+      if (NT == 1)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) xv[s % (NT == 1 ? 4 : 1)] = load_x(0, s);
       asm volatile("cp.async.wait_group %0;" ::"n"(W4_STAGES - 1) : "memory");
       __syncwarp();
       const uint8_t* st = ring + (size_t)slot * STAGE;
-      const uint4 sz = *reinterpret_cast<const uint4*>(st + MATS * W4_MAT_BYTES + lane * 16);
-      const uint32_t szv[4] = {sz.x, sz.y, sz.z, sz.w};
-      float grp[MATS][NT][4];
+      const uint4 sz = *reinterpret_cast<const uint4*>(st + 2 * W4_MAT_BYTES + lane * 16);
+      float grp[2][NT][4], xs[NT][4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {                  // 32 codes of each row
-        const int sub = s * sub_n / 4;               // the chunk's group they belong to
-        const bool starts = (s * sub_n) % 4 == 0, ends = ((s + 1) * sub_n) % 4 == 0;
+        constexpr int PER = 4 / SUBN;                // such steps in a group
         uint32_t xb[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const int k = c * W4_CHUNK + s * 32 + q * 8;
-          const uint4 v = xrow[t] && k < sg.K ? *(xrow[t] + k / 8) : make_uint4(0, 0, 0, 0);
-          xb[t][0] = __byte_perm(v.x, v.z, 0x5410);
-          xb[t][1] = __byte_perm(v.x, v.z, 0x7632);
-          xb[t][2] = __byte_perm(v.y, v.w, 0x5410);
-          xb[t][3] = __byte_perm(v.y, v.w, 0x7632);
+          if (t > 0 && t * 8 >= sg.rows) break;
+          const uint4 v = NT == 1 ? xv[s % (NT == 1 ? 4 : 1)] : load_x(t, s);
+          if (MATS == 2) {
+            xb[t][0] = __byte_perm(v.x, v.z, 0x5410);
+            xb[t][1] = __byte_perm(v.x, v.z, 0x7632);
+            xb[t][2] = __byte_perm(v.y, v.w, 0x5410);
+            xb[t][3] = __byte_perm(v.y, v.w, 0x7632);
+          } else {
+            xb[t][0] = v.x; xb[t][1] = v.y; xb[t][2] = v.z; xb[t][3] = v.w;
+          }
+          if (s % PER == 0) xs[t][0] = xs[t][1] = xs[t][2] = xs[t][3] = 0.0f;
+          mma_16816(xs[t], ones, xb[t][0], xb[t][1]);
+          mma_16816(xs[t], ones, xb[t][2], xb[t][3]);
         }
 #pragma unroll
-        for (int a = 0; a < MATS; ++a) {
-          const uint32_t zz = __shfl_sync(0xffffffffu, szv[2 + a], (lane & 28) | sub);
-          const uint32_t z0 = ((zz & 15u) | 0x4300u) * 0x00010001u, z1 = (((zz >> 16) & 15u) | 0x4300u) * 0x00010001u;
-          const uint8_t* w = st + a * W4_MAT_BYTES + g * 64 + ((s ^ ((g >> 1) & 3)) * 16) + q * 4;
+        for (int a = 0; a < 2; ++a) {
           uint32_t lo[4], hi[4];
-          unpack_w4(*reinterpret_cast<const uint32_t*>(w), z0, lo);
-          unpack_w4(*reinterpret_cast<const uint32_t*>(w + 512), z1, hi);
+          unpack_w4(*reinterpret_cast<const uint32_t*>(st + a * W4_MAT_BYTES + get[s]), lo);
+          unpack_w4(*reinterpret_cast<const uint32_t*>(st + a * W4_MAT_BYTES + get[s] + 512), hi);
           const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (t > 0 && t * 8 >= sg.rows) break;
-            if (starts) grp[a][t][0] = grp[a][t][1] = grp[a][t][2] = grp[a][t][3] = 0.0f;
+            if (s % PER == 0) grp[a][t][0] = grp[a][t][1] = grp[a][t][2] = grp[a][t][3] = 0.0f;
             mma_16816(grp[a][t], a0, xb[t][0], xb[t][1]);
             mma_16816(grp[a][t], a1, xb[t][2], xb[t][3]);
           }
-          if (ends) {
-            const uint32_t ss = __shfl_sync(0xffffffffu, szv[a], (lane & 28) | sub);
+          if ((s + 1) % PER == 0) {                  // the group's sum is whole
+            uint32_t ss = a ? sz.y : sz.x, zz = a ? sz.w : sz.z;
+            if (SUBN > 1) {
+              ss = __shfl_sync(0xffffffffu, ss, (lane & 28) | (s / PER));
+              zz = __shfl_sync(0xffffffffu, zz, (lane & 28) | (s / PER));
+            }
             const float s0 = __uint_as_float(ss << 16), s1 = __uint_as_float(ss & 0xffff0000u);
+            const float z0 = -128.0f - (float)(zz & 15u), z1 = -128.0f - (float)((zz >> 16) & 15u);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               if (t > 0 && t * 8 >= sg.rows) break;
-              acc[a][t][0] = fmaf(s0, grp[a][t][0], acc[a][t][0]);
-              acc[a][t][1] = fmaf(s0, grp[a][t][1], acc[a][t][1]);
-              acc[a][t][2] = fmaf(s1, grp[a][t][2], acc[a][t][2]);
-              acc[a][t][3] = fmaf(s1, grp[a][t][3], acc[a][t][3]);
+              acc[a][t][0] = fmaf(s0, fmaf(z0, xs[t][0], grp[a][t][0]), acc[a][t][0]);
+              acc[a][t][1] = fmaf(s0, fmaf(z0, xs[t][1], grp[a][t][1]), acc[a][t][1]);
+              acc[a][t][2] = fmaf(s1, fmaf(z1, xs[t][0], grp[a][t][2]), acc[a][t][2]);
+              acc[a][t][3] = fmaf(s1, fmaf(z1, xs[t][1], grp[a][t][3]), acc[a][t][3]);
             }
           }
         }
@@ -320,29 +367,30 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
     }
     // ------------------------------------------- the K shares meet, epilogue
 #pragma unroll
-    for (int a = 0; a < MATS; ++a)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         red[warp * RED + (a * NT + t) * 32 + lane] =
             make_float4(acc[a][t][0], acc[a][t][1], acc[a][t][2], acc[a][t][3]);
     __syncthreads();
-    const int mu = m0 - wm * 16;                     // the unit's first weight row
+    const int mu = m0 - wm * WROWS;                  // the unit's first weight row
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sg.dense ? p.out_s : p.out);
     const float* redf = reinterpret_cast<const float*>(red);
     for (int i = tid; i < sg.rows * unit_rows; i += W4_THREADS) {
       const int n = i / unit_rows, m = i - n * unit_rows;
       if (mu + m >= sg.M) continue;
-      const int r = m & 15;
+      const int r = m & 15, a = MATS == 1 ? (m >> 4) & 1 : 0, w0 = m / WROWS * WK;
       const int at = ((n >> 3) * 32 + (r & 7) * 4 + ((n & 7) >> 1)) * 4 + (r >> 3) * 2 + (n & 1);
-      float v[MATS];
-#pragma unroll
-      for (int a = 0; a < MATS; ++a) {
-        v[a] = 0.0f;
-        for (int w = 0; w < WK; ++w) v[a] += redf[((m >> 4) * WK + w) * RED * 4 + a * NT * 128 + at];
+      float v[2] = {0.0f, 0.0f};
+      for (int w = 0; w < WK; ++w) {
+        v[0] += redf[((w0 + w) * RED + a * NT * 32) * 4 + at];
+        if (MATS == 2) v[1] += redf[((w0 + w) * RED + NT * 32) * 4 + at];
       }
       // One rounding, of the activation (gate/up) or of the result (down).
-      const float o = MATS == 2 ? v[0] / (1.0f + __expf(-v[0])) * v[MATS - 1] : v[0];
-      out[(size_t)(sg.t0 + n) * sg.M + mu + m] = __float2bfloat16_rn(o);
+      const float o = MATS == 2 ? v[0] / (1.0f + __expf(-v[0])) * v[1] : v[0];
+      int col = mu + m;
+      if (MATS == 2) col = (col & ~7) | ((col & 3) * 2 + ((col >> 2) & 1));   // h in the down product's order of k
+      out[(size_t)(sg.t0 + n) * sg.M + col] = __float2bfloat16_rn(o);
     }
     __syncthreads();
   }
@@ -362,22 +410,49 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
   }
 }
 
-template <int MATS, int NT> int w4_smem_bytes(int n_seg) {
-  return W4_WARPS * (w4_stages<NT>() * (MATS * W4_MAT_BYTES + W4_SC_BYTES) + MATS * NT * 512) +
-         n_seg * (int)sizeof(W4Entry);
+template <int NT> int w4_smem_bytes(int n_seg) {
+  return W4_WARPS * (w4_stages<NT>() * (2 * W4_MAT_BYTES + W4_SC_BYTES) + 2 * NT * 512) + n_seg * (int)sizeof(W4Entry);
+}
+
+// Experts that a batch is expected to touch under even routing.
+double w4_touched(const W4GemmParams& p) {
+  if (p.n_routed <= 0 || p.max_rows <= 0) return 0.0;
+  return p.n_routed * (1.0 - pow(1.0 - 1.0 / p.n_routed, (double)p.max_rows));
+}
+
+// Token tiles of eight per unit. A segment with more rows takes its weights
+// again for every 8 NT of them, a unit with more tiles does more products per
+// weight: 1, 1.3 and 2.1 times the time of one tile, measured at d = 7168 with
+// 8, 16 and 32 rows an expert. Routed segments vary about their mean.
+int w4_token_tiles(const W4GemmParams& p) {
+  const double act = w4_touched(p), cost[3] = {1.0, 1.3, 2.1};
+  int best = 1;
+  double least = 1e300;
+  for (int i = 0; i < 3; ++i) {
+    const int nt = 1 << i;
+    double t = (double)p.M_s * p.K_s * ceil_div(p.dense_rows, 8 * nt);
+    if (act > 0.0) {
+      const double mean = p.max_rows / act, passes = (mean + sqrt(mean)) / (8.0 * nt);
+      t += act * p.M * p.K * (passes > 1.0 ? passes : 1.0);
+    }
+    t *= cost[i];
+    if (t < least) {
+      least = t;
+      best = nt;
+    }
+  }
+  return best;
 }
 
 // Warps along K. A CTA's time is its units times a warp's chunks in each (and
 // about half a chunk of joining the shares); the split that makes this
 // smallest for the experts that the batch is expected to touch wins.
 int w4_split(const W4GemmParams& p, int slots) {
-  double act = 0.0;
-  if (p.n_routed > 0 && p.max_rows > 0)
-    act = p.n_routed * (1.0 - pow(1.0 - 1.0 / p.n_routed, (double)p.max_rows));
+  const double act = w4_touched(p);
   int best = 1;
   double least = 1e300;
   for (int wk = 1; wk <= W4_WARPS; wk *= 2) {
-    const int rows = 16 * (W4_WARPS / wk);
+    const int rows = (p.mats == 2 ? 16 : 32) * (W4_WARPS / wk);
     const double units = act * ceil_div(p.M, rows) + (p.dense_rows > 0 ? ceil_div(p.M_s, rows) : 0);
     const int K = p.n_routed > 0 ? p.K : p.K_s;
     const double t = ceil(units / slots) * (ceil_div(ceil_div(K, W4_CHUNK), wk) + 0.5);
@@ -420,8 +495,9 @@ template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16*
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// scale = (largest magnitude) / 7 with the codes centred on 8, or (max - min)
-// / 15 with a zero point, rounded to bf16 before the codes are taken: the
+// scale = (largest magnitude) * (1/7) with the codes centred on 8, or (max -
+// min) * (1/15) with a zero point, the factors and products in fp32; it is
+// rounded to bf16 before the codes are taken: the
 // rounding costs no accuracy. A group of zeros gets scale 0; one that holds a
 // value that is not finite gets a NaN scale, so that it shows.
 template <typename T>
@@ -452,7 +528,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ 
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       odd |= __shfl_xor_sync(0xffffffffu, odd, o);
     }
-    const __nv_bfloat16 s16 = __float2bfloat16_rn(zero ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f);
+    const __nv_bfloat16 s16 = __float2bfloat16_rn(zero ? (hi - lo) * (1.0f / 15.0f) : fmaxf(hi, -lo) * (1.0f / 7.0f));
     const float s = __bfloat162float(s16), step = s > 0.0f ? s : 1.0f;
     const float z = zero ? fminf(fmaxf(rintf(-lo / step), 0.0f), 15.0f) : 8.0f;
     uint32_t word = 0;
@@ -492,12 +568,7 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __re
 
 cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
   const int slots = 2 * num_sms;
-  // Token rows a unit takes: its segments' mean, with room for the uneven
-  // ones (more rows run as further passes over the unit's weights).
-  const double mean = p.n_routed > 0 ? (double)p.max_rows / p.n_routed : 0.0;
-  const double want = mean > 0.0 ? 2.0 * mean + 2.0 : 0.0;
-  const double rows = want > p.dense_rows ? want : p.dense_rows;
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  const int nt = w4_token_tiles(p);
   const int wk = w4_split(p, slots);
   const int n_seg = p.n_routed + (p.dense_rows > 0 ? 1 : 0);
   auto go = [&](auto kernel, int smem) {
@@ -515,13 +586,19 @@ cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
     cfg.numAttrs = p.wait_previous ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, p, wk);
   };
-  if (p.mats == 2)
-    return nt == 1   ? go(w4_gemm_kernel<2, 1>, w4_smem_bytes<2, 1>(n_seg))
-           : nt == 2 ? go(w4_gemm_kernel<2, 2>, w4_smem_bytes<2, 2>(n_seg))
-                     : go(w4_gemm_kernel<2, 4>, w4_smem_bytes<2, 4>(n_seg));
-  return nt == 1   ? go(w4_gemm_kernel<1, 1>, w4_smem_bytes<1, 1>(n_seg))
-         : nt == 2 ? go(w4_gemm_kernel<1, 2>, w4_smem_bytes<1, 2>(n_seg))
-                   : go(w4_gemm_kernel<1, 4>, w4_smem_bytes<1, 4>(n_seg));
+  auto with = [&](auto mats, auto n) {
+    constexpr int M = decltype(mats)::value, N = decltype(n)::value;
+    const int smem = w4_smem_bytes<N>(n_seg);
+    return p.group == 128  ? go(w4_gemm_kernel<M, N, 1>, smem)
+           : p.group == 64 ? go(w4_gemm_kernel<M, N, 2>, smem)
+                           : go(w4_gemm_kernel<M, N, 4>, smem);
+  };
+  auto rows_of = [&](auto n) {
+    return p.mats == 2 ? with(std::integral_constant<int, 2>{}, n) : with(std::integral_constant<int, 1>{}, n);
+  };
+  return nt == 1   ? rows_of(std::integral_constant<int, 1>{})
+         : nt == 2 ? rows_of(std::integral_constant<int, 2>{})
+                   : rows_of(std::integral_constant<int, 4>{});
 }
 
 cudaError_t launch_w4_quantize(int dtype, const void* w, long long n, int group, void* q, void* scale, void* zero,

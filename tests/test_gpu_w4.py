@@ -1,10 +1,11 @@
 """4-bit expert weights on the GPU against the fp64 oracle.
 
-Bounds of the expert FFN. Codes minus zero points are exact small integers and
-the activations are bf16, so every product inside a group is exact; what the
-tensor cores add and the fp32 scaling afterwards are off by at most one unit
-of 2^-23 (the adder may truncate) of the absolute terms per addition, at most
-K / 16 + 16 of them in a row. SiLU's slope is below 1.1, its fp32 evaluation
+Bounds of the expert FFN. The products run over 128 + code, exact in bf16, and
+128 + zero times the group's sum of activations comes off in fp32: every
+product is exact, and each addition is off by at most one unit of 2^-23 (the
+tensor cores' adder may truncate) of the absolute terms. A group's two sums
+have terms of at most 143 |x| and G / 16 + 4 additions in a row; their
+difference, scaled, takes at most K / 16 + 16 more over |W| |x|. SiLU's slope is below 1.1, its fp32 evaluation
 good to 2^-20. The intermediate is rounded to bf16 (2^-8 of its size at most),
 passes through |W2|, and the result is rounded once more.
 
@@ -39,11 +40,11 @@ def quantize_rule(w, group, zeros):
     g = w.cpu().float().unflatten(-1, (-1, group))
     if zeros:
         lo_, hi = g.amin(-1, keepdim=True).clamp(max=0), g.amax(-1, keepdim=True).clamp(min=0)
-        scale = ((hi - lo_) / 15.0).to(BF)
+        scale = ((hi - lo_) * torch.tensor(1.0 / 15.0, dtype=torch.float32)).to(BF)
         step = torch.where(scale > 0, scale.float(), 1.0)
         zero = torch.round(-lo_ / step).clamp(0, 15)
     else:
-        scale = (g.abs().amax(-1, keepdim=True) / 7.0).to(BF)
+        scale = (g.abs().amax(-1, keepdim=True) * torch.tensor(1.0 / 7.0, dtype=torch.float32)).to(BF)
         step = torch.where(scale > 0, scale.float(), 1.0)
         zero = torch.full_like(step, 8.0)
     code = (torch.round(g / step) + zero).clamp(0, 15)
@@ -120,13 +121,19 @@ def make(T, d, E, k, f, fs, group, zeros, seed=0, skew=0.0):
     return cfg, x, w, ws, perm_src, offsets
 
 
-def check_rows(got, x, w1, w3, w2, what):
+def scales(m, e=None):
+    """The scale of every weight."""
+    return np.repeat(f64(m.scale if e is None else m.scale[e]), m.group, axis=-1)
+
+
+def check_rows(got, x, w1, w3, w2, what, s1, s3, s2, group):
     y, a, b, h = lo.swiglu_rows(x, w1, w3, w2)
     units = lambda K: (K / 16 + 16) * 2.0 ** -23
     K, f = x.shape[1], h.shape[1]
-    ea, eb = units(K) * (np.abs(x) @ np.abs(w1).T), units(K) * (np.abs(x) @ np.abs(w3).T)
+    in_group = (group / 16 + 4) * 2.0 ** -23 * 2 * 143
+    ea, eb = (units(K) * (np.abs(x) @ np.abs(w).T) + in_group * (np.abs(x) @ s.T) for w, s in ((w1, s1), (w3, s3)))
     eh = 1.1 * ea * (np.abs(b) + eb) + np.abs(h) / np.maximum(np.abs(b), 1e-300) * eb + (2.0 ** -8 + 2.0 ** -20) * np.abs(h)
-    ey = eh @ np.abs(w2).T + units(f) * (np.abs(h) @ np.abs(w2).T) + 2.0 ** -8 * np.abs(y) + 1e-38
+    ey = eh @ np.abs(w2).T + units(f) * (np.abs(h) @ np.abs(w2).T) + in_group * (np.abs(h) @ s2.T) + 2.0 ** -8 * np.abs(y) + 1e-38
     got = f64(got)
     assert np.isfinite(got).all(), what
     assert (np.abs(got - y) <= ey).all(), (what, (np.abs(got - y) - ey).max())
@@ -150,9 +157,10 @@ def check_experts(cfg, x, w, ws, perm_src, offsets, y, ys, experts=None):
     off, xp = offsets.tolist(), f64(x)[perm_src.cpu().numpy()]
     for e in range(cfg.E) if experts is None else experts:
         if off[e] < off[e + 1]:
-            check_rows(y[off[e]:off[e + 1]], xp[off[e]:off[e + 1]], *[dense(m, e) for m in w], f"expert {e}")
+            check_rows(y[off[e]:off[e + 1]], xp[off[e]:off[e + 1]], *[dense(m, e) for m in w], f"expert {e}",
+                       *[scales(m, e) for m in w], w[0].group)
     if ys is not None:
-        check_rows(ys, f64(x), *[dense(m) for m in ws], "shared")
+        check_rows(ys, f64(x), *[dense(m) for m in ws], "shared", *[scales(m) for m in ws], w[0].group)
 
 
 CASES = [  # T, d, E, k, f, f_shared, group, zeros
