@@ -860,6 +860,7 @@ moe_status enqueue_experts_w4(const moe_config& c, int group, const void* x, con
   }
   g.err = at<uint32_t>(ws, L.err);
   g.err_keep = err_keep;
+  g.has_zero = w1->zero || w3->zero || (shared && (ws1->zero || ws3->zero));
   MOE_CUDA(launch_w4_gemm(g, device_sm_count(), s));
   W4GemmParams q = {};
   q.mats = 1;
@@ -877,6 +878,7 @@ moe_status enqueue_experts_w4(const moe_config& c, int group, const void* x, con
     q.out_s = y_sh;
     q.w_s[0] = w4_operand(ws2);
   }
+  q.has_zero = w2->zero || (shared && ws2->zero);
   q.wait_previous = 1;
   MOE_CUDA(launch_w4_gemm(q, device_sm_count(), s));
   return MOE_OK;

@@ -266,6 +266,7 @@ struct W4GemmParams {
   int dense_rows, M_s, K_s; // the shared expert, 0 rows: none
   const void* x_s; void* out_s;
   W4Operand w[2], w_s[2];
+  int has_zero;             // some operand has zero points
   uint32_t* err;            // or null: no check of offsets and gather
   int err_keep;             // add to the word what earlier kernels of the call left in it
   int wait_previous;        // start early, wait for the launch before (programmatic dependence)

@@ -30,7 +30,7 @@
 //
 // Layout of the work: a CTA of 8 warps takes a contiguous run of units; a unit
 // is 16 WM rows of W1 and W3 (32 WM rows of W2) of one expert times up to 8 NT
-// of its token rows, its K split over WK = 8 / WM warps in chunks of 128, two
+// of its token rows, its K split over WK = 8 / WM warps in chunks of 256, two
 // 16-row tiles a warp, which share the token fragments. Each warp streams its
 // chunks through a ring of cp.async stages of its own, across unit boundaries,
 // so weights keep flowing while a unit's partial sums meet in shared memory.
@@ -45,11 +45,10 @@ namespace {
 
 constexpr int W4_WARPS = 8;
 constexpr int W4_THREADS = W4_WARPS * 32;
-// Ring stages: with 32 token rows a unit the partial sums take a stage's room.
-template <int NT> constexpr int w4_stages() { return NT == 4 ? 3 : 4; }
-constexpr int W4_CHUNK = 128;                       // k of one ring stage
-constexpr int W4_MAT_BYTES = 16 * W4_CHUNK / 2;     // 16 rows of codes
-constexpr int W4_SC_BYTES = 32 * 16;                // scales and zeros, 16 bytes a lane
+constexpr int W4_CHUNK = 256;                       // k of one ring stage
+constexpr int W4_TILE_BYTES = 16 * W4_CHUNK / 2;    // 16 rows of codes
+constexpr int W4_STAGE_BYTES = 2 * W4_TILE_BYTES;
+constexpr int W4_STAGES = 2;
 
 __device__ __forceinline__ uint32_t w4_smem(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -57,6 +56,16 @@ __device__ __forceinline__ uint32_t w4_smem(const void* p) {
 // 16 bytes, or zeros where !valid (nothing is read then).
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// c = a b, and c += a b.
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -83,12 +92,9 @@ struct W4Seg {   // one segment's share of a unit
 using W4Entry = int4;
 
 // MATS = 2: gate/up, the two tiles of a warp are the same rows of W1 and W3.
-// MATS = 1: down, they are 16 rows of W2 and the 16 after them. SUBN: groups
-// in a chunk of 128.
-template <int MATS, int NT, int SUBN>
+// MATS = 1: down, they are 16 rows of W2 and the 16 after them.
+template <int MATS, int NT, int GROUP>
 __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmParams p, int WK) {
-  constexpr int W4_STAGES = w4_stages<NT>();
-  constexpr int STAGE = 2 * W4_MAT_BYTES + W4_SC_BYTES;
   constexpr int RED = 2 * NT * 32;                        // float4s of one warp's partial sums
   constexpr int WROWS = MATS == 2 ? 16 : 32;              // weight rows of a warp
   extern __shared__ __align__(128) uint8_t w4_dyn[];
@@ -96,8 +102,8 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
   __shared__ long long warp_u[W4_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int WM = W4_WARPS / WK, wk = warp % WK, wm = warp / WK;
-  uint8_t* ring = w4_dyn + (size_t)warp * W4_STAGES * STAGE;
-  float4* red = reinterpret_cast<float4*>(w4_dyn + (size_t)W4_WARPS * W4_STAGES * STAGE);
+  uint8_t* ring = w4_dyn + (size_t)warp * W4_STAGES * W4_STAGE_BYTES;
+  float4* red = reinterpret_cast<float4*>(w4_dyn + (size_t)W4_WARPS * W4_STAGES * W4_STAGE_BYTES);
   W4Entry* tab = reinterpret_cast<W4Entry*>(red + W4_WARPS * RED);
 
   // -------------------------------------------------- the segments' table
@@ -183,16 +189,15 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
   }
 
   // ------------------------------------------------------- weight stream
+  constexpr int NG = W4_CHUNK / GROUP;               // groups of a chunk: 2, 4 or 8
+  constexpr int PER = GROUP / 32;                    // steps of 32 k in a group
+  constexpr int HELD = NG > 4 ? 2 : 1;               // scales of a row that a lane loads: 4 lanes share a row's
   int pu = u0, phint = first_seg, pc = 0, pn = 0, pK = 0, pgroups = 0;   // the next chunk: unit, index, count
-  const uint8_t* pq[2] = {nullptr, nullptr};         // this lane's 16 codes bytes of row g, per tile
+  const uint8_t* pq[2] = {nullptr, nullptr};         // this lane's pieces of codes, per tile
   const uint16_t* psc[2] = {nullptr, nullptr};       // row g's scales
   const uint8_t* pz[2] = {nullptr, nullptr};         // and zero points, or null
-  bool p_ok[2] = {false, false};                     // the tile lies inside the matrix (M is a multiple of 32)
-  uint16_t sc_r[2][2];
-  uint8_t z_r[2][2];
-  int sc_slot = -1;                                  // stage that the loaded scales belong to
-#pragma unroll
-  for (int a = 0; a < 2; ++a) sc_r[a][0] = sc_r[a][1] = z_r[a][0] = z_r[a][1] = 0;
+  uint16_t sc_r[2][2][HELD];                         // scales of the chunk under way: rows g and g + 8
+  uint8_t z_r[2][2][HELD];
 
   auto open_unit = [&]() {                           // pointers of unit pu
     W4Seg sg;
@@ -200,73 +205,79 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
     locate(pu, phint, sg, m0);
     pK = sg.K;
     pn = ceil_div(sg.K, W4_CHUNK);
-    pgroups = sg.K / p.group;
+    pgroups = sg.K / GROUP;
     pc = wk;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       const W4Operand& op = sg.op[MATS == 2 ? a : 0];
-      const int m = MATS == 2 ? m0 : m0 + 16 * a;
-      p_ok[a] = m < sg.M;
-      const size_t row = sg.row0 + (p_ok[a] ? m + g : 0);
-      pq[a] = op.q + row * (size_t)(sg.K / 2) + q * 16;
-      psc[a] = static_cast<const uint16_t*>(op.scale) + row * pgroups;
-      pz[a] = op.zero ? op.zero + row * pgroups : nullptr;
+      // A tile past the matrix (M is a multiple of 32) reads the first one: its
+      // products are not stored.
+      int m = MATS == 2 ? m0 : m0 + 16 * a;
+      if (m >= sg.M) m = 0;
+      const size_t row = sg.row0 + m;
+      pq[a] = op.q + (row + (lane >> 3)) * (size_t)(sg.K / 2) + (lane & 7) * 16 + pc * (W4_CHUNK / 2);
+      psc[a] = static_cast<const uint16_t*>(op.scale) + (row + g) * pgroups;
+      pz[a] = op.zero ? op.zero + (row + g) * pgroups : nullptr;
     }
   };
-  auto store_scales = [&]() {
-    if (sc_slot < 0) return;
-    *reinterpret_cast<uint4*>(ring + (size_t)sc_slot * STAGE + 2 * W4_MAT_BYTES + lane * 16) =
-        make_uint4((uint32_t)sc_r[0][0] | ((uint32_t)sc_r[0][1] << 16), (uint32_t)sc_r[1][0] | ((uint32_t)sc_r[1][1] << 16),
-                   (uint32_t)z_r[0][0] | ((uint32_t)z_r[0][1] << 16), (uint32_t)z_r[1][0] | ((uint32_t)z_r[1][1] << 16));
-    sc_slot = -1;
-  };
-  // Where this lane's pieces of a tile go in a stage: 64 bytes a row, its
-  // 16-byte pieces swapped about so that the word reads below and these
-  // writes each take every bank once.
-  const uint32_t ring_s = w4_smem(ring), put = g * 64 + ((q ^ ((g >> 1) & 3)) * 16);
-  // Start the next chunk of this warp's stream into stage `slot`. Its scales
-  // come by plain loads and are put into the stage at the next call, when
-  // they have arrived.
+  // A tile in a stage: 128 bytes a row, its 16-byte pieces swapped about so
+  // that these writes and the word reads below each take every bank once.
+  const uint32_t ring_s = w4_smem(ring);
+  uint32_t put[2];                                   // rows lane / 8 + 8 i, and + 4
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = (lane >> 3) + 4 * h;
+    put[h] = r * 128 + (((lane & 7) ^ r) * 16);
+  }
+  // Start the next chunk of this warp's stream into stage `slot`: codes into
+  // shared memory, scales into registers, both used one chunk later.
   auto issue = [&](int slot) {
-    store_scales();
     while (pu < u1 && pc >= pn) {
       if (++pu < u1) open_unit();
     }
     if (pu < u1) {
-      const uint32_t dst = ring_s + slot * STAGE + put;
-      const bool in_k = pc * W4_CHUNK + q * 32 < pK;
-      const int gi = min(pc * SUBN + (q & (SUBN - 1)), pgroups - 1);
-      const size_t row8 = (size_t)pK * 4;            // eight rows of codes
+      const uint32_t dst = ring_s + slot * W4_STAGE_BYTES;
+      const size_t row4 = (size_t)pK * 2;            // four rows of codes
+      if ((pc + 1) * W4_CHUNK <= pK) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp_async16_all(dst + a * W4_TILE_BYTES + (i >> 1) * 1024 + put[i & 1], pq[a] + i * row4);
+      } else {                                       // K ends inside the chunk
+        const bool in_k = pc * W4_CHUNK + (lane & 7) * 32 < pK;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp_async16_zfill(dst + a * W4_TILE_BYTES + (i >> 1) * 1024 + put[i & 1], pq[a] + i * row4 - (in_k ? 0 : (lane & 7) * 16), in_k);
+      }
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const bool ok = p_ok[a] && in_k;
-        const uint8_t* src = ok ? pq[a] + pc * (W4_CHUNK / 2) : pq[a] - q * 16;
-        cp_async16_zfill(dst + a * W4_MAT_BYTES, src, ok);
-        cp_async16_zfill(dst + a * W4_MAT_BYTES + 512, ok ? src + row8 : src, ok);
-        const int g8 = p_ok[a] ? 8 * pgroups : 0;
-        sc_r[a][0] = __ldg(psc[a] + gi);
-        sc_r[a][1] = __ldg(psc[a] + gi + g8);
-        if (pz[a]) {
-          z_r[a][0] = __ldg(pz[a] + gi);
-          z_r[a][1] = __ldg(pz[a] + gi + g8);
-        } else {
-          z_r[a][0] = z_r[a][1] = 8;
+        pq[a] += WK * (W4_CHUNK / 2);
+#pragma unroll
+        for (int e = 0; e < HELD; ++e) {
+          const int gi = min(pc * NG + (q & (NG / HELD - 1)) * HELD + e, pgroups - 1);
+          sc_r[a][0][e] = __ldg(psc[a] + gi);
+          sc_r[a][1][e] = __ldg(psc[a] + gi + 8 * pgroups);
+          z_r[a][0][e] = z_r[a][1][e] = 8;
+          if (pz[a]) {
+            z_r[a][0][e] = __ldg(pz[a] + gi);
+            z_r[a][1][e] = __ldg(pz[a] + gi + 8 * pgroups);
+          }
         }
       }
-      sc_slot = slot;
       pc += WK;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   if (pu < u1) open_unit();
-  for (int i = 0; i < W4_STAGES - 1; ++i) issue(i);
+  issue(0);
   if (p.wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ------------------------------------------------------------- products
   const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-  uint32_t get[4];                                   // word s * 4 + q of row g in a stage
-#pragma unroll
-  for (int s = 0; s < 4; ++s) get[s] = g * 64 + ((s ^ ((g >> 1) & 3)) * 16) + q * 4;
+  const uint32_t get = g * 128 + q * 4;              // word q of row g's piece s: ^ (s ^ g) * 16
   int slot = 0, hint = first_seg;
   for (int u = u0; u < u1; ++u) {
     W4Seg sg;
@@ -275,17 +286,16 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
     const uint4* xrow[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = t * 8 + g;
-      xrow[t] = nullptr;
-      if (r < sg.rows) {
-        size_t src = sg.t0 + r;
-        if (!sg.dense && p.gather) {
-          const int v = p.gather[sg.t0 + r];
-          src = v >= 0 && v < p.gather_rows ? v : 0;
-        }
-        xrow[t] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s : p.x) +
-                                                 src * (size_t)sg.K) + q;
+      // Token columns past the segment's rows read its first row: a column of
+      // the product takes nothing from its neighbours, and these are not stored.
+      const int r = t * 8 + g < sg.rows ? t * 8 + g : 0;
+      size_t src = sg.t0 + r;
+      if (!sg.dense && p.gather) {
+        const int v = p.gather[sg.t0 + r];
+        src = v >= 0 && v < p.gather_rows ? v : 0;
       }
+      xrow[t] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s : p.x) +
+                                               src * (size_t)sg.K) + q;
     }
     float acc[2][NT][4];
 #pragma unroll
@@ -296,28 +306,37 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
         for (int i = 0; i < 4; ++i) acc[a][t][i] = 0.0f;
     const int nch = ceil_div(sg.K, W4_CHUNK);
     for (int c = wk; c < nch; c += WK) {
-      issue(slot == 0 ? W4_STAGES - 1 : slot - 1);
+      uint32_t sc[2][HELD], zp[2][HELD];
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < HELD; ++e) {
+          sc[a][e] = (uint32_t)sc_r[a][0][e] | ((uint32_t)sc_r[a][1][e] << 16);
+          zp[a][e] = (uint32_t)z_r[a][0][e] | ((uint32_t)z_r[a][1][e] << 16);
+        }
+      issue(slot ^ 1);
+      const bool whole = (c + 1) * W4_CHUNK <= sg.K;
       auto load_x = [&](int t, int s) -> uint4 {     // eight k of a token row
-        const int k32 = c * 4 + s;
-        return xrow[t] && k32 * 32 < sg.K ? *(xrow[t] + k32 * 4) : make_uint4(0, 0, 0, 0);
+        if (whole) return xrow[t][c * (W4_CHUNK / 8) + s * 4];
+        return c * W4_CHUNK + s * 32 < sg.K ? xrow[t][c * (W4_CHUNK / 8) + s * 4] : make_uint4(0, 0, 0, 0);
       };
-      uint4 xv[NT == 1 ? 4 : 1];                     // with one token tile: fetched before the wait
+      constexpr int AHEAD = NT == 1 ? 4 : 1;         // steps whose token rows are fetched ahead
+      uint4 xv[AHEAD];
       if (NT == 1)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) xv[s % (NT == 1 ? 4 : 1)] = load_x(0, s);
-      asm volatile("cp.async.wait_group %0;" ::"n"(W4_STAGES - 1) : "memory");
+        for (int s = 0; s < AHEAD; ++s) xv[s] = load_x(0, s);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncwarp();
-      const uint8_t* st = ring + (size_t)slot * STAGE;
-      const uint4 sz = *reinterpret_cast<const uint4*>(st + 2 * W4_MAT_BYTES + lane * 16);
+      const uint8_t* st = ring + slot * W4_STAGE_BYTES;
       float grp[2][NT][4], xs[NT][4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {                  // 32 codes of each row
-        constexpr int PER = 4 / SUBN;                // such steps in a group
+      for (int s = 0; s < W4_CHUNK / 32; ++s) {      // 32 codes of each row
         uint32_t xb[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           if (t > 0 && t * 8 >= sg.rows) break;
-          const uint4 v = NT == 1 ? xv[s % (NT == 1 ? 4 : 1)] : load_x(t, s);
+          const uint4 v = NT == 1 ? xv[s % AHEAD] : load_x(t, s);
+          if (NT == 1 && s + AHEAD < W4_CHUNK / 32) xv[s % AHEAD] = load_x(0, s + AHEAD);
           if (MATS == 2) {
             xb[t][0] = __byte_perm(v.x, v.z, 0x5410);
             xb[t][1] = __byte_perm(v.x, v.z, 0x7632);
@@ -326,31 +345,34 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
           } else {
             xb[t][0] = v.x; xb[t][1] = v.y; xb[t][2] = v.z; xb[t][3] = v.w;
           }
-          if (s % PER == 0) xs[t][0] = xs[t][1] = xs[t][2] = xs[t][3] = 0.0f;
-          mma_16816(xs[t], ones, xb[t][0], xb[t][1]);
+          if (s % PER == 0) mma_16816_first(xs[t], ones, xb[t][0], xb[t][1]);
+          else mma_16816(xs[t], ones, xb[t][0], xb[t][1]);
           mma_16816(xs[t], ones, xb[t][2], xb[t][3]);
         }
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
+          const uint8_t* w = st + a * W4_TILE_BYTES + (get ^ ((s ^ g) * 16));
           uint32_t lo[4], hi[4];
-          unpack_w4(*reinterpret_cast<const uint32_t*>(st + a * W4_MAT_BYTES + get[s]), lo);
-          unpack_w4(*reinterpret_cast<const uint32_t*>(st + a * W4_MAT_BYTES + get[s] + 512), hi);
+          unpack_w4(*reinterpret_cast<const uint32_t*>(w), lo);
+          unpack_w4(*reinterpret_cast<const uint32_t*>(w + 1024), hi);
           const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if (t > 0 && t * 8 >= sg.rows) break;
-            if (s % PER == 0) grp[a][t][0] = grp[a][t][1] = grp[a][t][2] = grp[a][t][3] = 0.0f;
-            mma_16816(grp[a][t], a0, xb[t][0], xb[t][1]);
+            if (s % PER == 0) mma_16816_first(grp[a][t], a0, xb[t][0], xb[t][1]);
+            else mma_16816(grp[a][t], a0, xb[t][0], xb[t][1]);
             mma_16816(grp[a][t], a1, xb[t][2], xb[t][3]);
           }
-          if ((s + 1) % PER == 0) {                  // the group's sum is whole
-            uint32_t ss = a ? sz.y : sz.x, zz = a ? sz.w : sz.z;
-            if (SUBN > 1) {
-              ss = __shfl_sync(0xffffffffu, ss, (lane & 28) | (s / PER));
-              zz = __shfl_sync(0xffffffffu, zz, (lane & 28) | (s / PER));
+          if ((s + 1) % PER == 0) {                  // the group's sum is whole: its scale, from the lane that has it
+            const int sub = s / PER;
+            const uint32_t ss = __shfl_sync(0xffffffffu, sc[a][sub % HELD], (lane & 28) | (sub / HELD));
+            float z0 = -136.0f, z1 = -136.0f;
+            if (p.has_zero) {
+              const uint32_t zz = __shfl_sync(0xffffffffu, zp[a][sub % HELD], (lane & 28) | (sub / HELD));
+              z0 = -128.0f - (float)(zz & 15u);
+              z1 = -128.0f - (float)((zz >> 16) & 15u);
             }
             const float s0 = __uint_as_float(ss << 16), s1 = __uint_as_float(ss & 0xffff0000u);
-            const float z0 = -128.0f - (float)(zz & 15u), z1 = -128.0f - (float)((zz >> 16) & 15u);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               if (t > 0 && t * 8 >= sg.rows) break;
@@ -363,7 +385,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
         }
       }
       __syncwarp();                                  // every lane has read the stage
-      if (++slot == W4_STAGES) slot = 0;
+      slot ^= 1;
     }
     // ------------------------------------------- the K shares meet, epilogue
 #pragma unroll
@@ -411,7 +433,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
 }
 
 template <int NT> int w4_smem_bytes(int n_seg) {
-  return W4_WARPS * (w4_stages<NT>() * (2 * W4_MAT_BYTES + W4_SC_BYTES) + 2 * NT * 512) + n_seg * (int)sizeof(W4Entry);
+  return W4_WARPS * (W4_STAGES * W4_STAGE_BYTES + 2 * NT * 512) + n_seg * (int)sizeof(W4Entry);
 }
 
 // Experts that a batch is expected to touch under even routing.
@@ -589,9 +611,9 @@ cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
   auto with = [&](auto mats, auto n) {
     constexpr int M = decltype(mats)::value, N = decltype(n)::value;
     const int smem = w4_smem_bytes<N>(n_seg);
-    return p.group == 128  ? go(w4_gemm_kernel<M, N, 1>, smem)
-           : p.group == 64 ? go(w4_gemm_kernel<M, N, 2>, smem)
-                           : go(w4_gemm_kernel<M, N, 4>, smem);
+    return p.group == 128  ? go(w4_gemm_kernel<M, N, 128>, smem)
+           : p.group == 64 ? go(w4_gemm_kernel<M, N, 64>, smem)
+                           : go(w4_gemm_kernel<M, N, 32>, smem);
   };
   auto rows_of = [&](auto n) {
     return p.mats == 2 ? with(std::integral_constant<int, 2>{}, n) : with(std::integral_constant<int, 1>{}, n);
