@@ -23,11 +23,12 @@
 //
 // Both kernels are bound by HBM: forward 4 T d elements, backward 6 T d. A CTA
 // owns whole rows, each thread the same 16-byte vectors of every row, so a row
-// crosses HBM once in each direction and stays in registers over both of its
-// reductions. Rows arrive through a ring of cp.async stages in shared memory
-// that is private to each thread (it reads only what it copied itself): the
-// loads of the next rows run on while a row's block reductions wait, without
-// registers for them and without a barrier.
+// crosses HBM once in each direction. Rows arrive through a ring of cp.async
+// stages in shared memory that is private to each thread (it reads only what
+// it copied itself): loads run ahead without registers and without a barrier.
+// Each row needs two sums over the block one after the other (y's, then the
+// stream's; in the backward the stream's and y's squares, then the branch's);
+// the second of one row and the first of the next share a barrier.
 //
 // Weight gradients: in the backward each CTA takes a contiguous run of rows
 // and keeps fp32 sums in registers; the runs' sums are added in run order by a
@@ -39,7 +40,8 @@
 namespace moe {
 namespace {
 
-constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMaxThreads = 512;    // forward: two 16-byte vectors a thread, four past 16 KB rows
+constexpr int kNormBwdThreads = 512;
 constexpr int kNormMaxStages = 4;
 
 template <typename T> __device__ __forceinline__ void unpack16(const uint4& v, float (&f)[Vec16<T>::N]);
@@ -84,42 +86,76 @@ __device__ __forceinline__ void cp_async_wait(int pending) {
   }
 }
 
-// Sum of N values over the block, the same bits in every thread. `buf`
+// Sums of four values over the block, the same bits in every thread. `buf`
 // alternates between calls: the barrier of one call separates the reads of
-// the call before it from the writes of the call after it.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* red, int& buf) {
+// the call before it from the writes of the call after it. Within a warp the
+// four are reduced together (each exchange halves the values a lane holds): 6
+// shuffles instead of 20, and as many again over the warps' sums.
+__device__ __forceinline__ void block_sum4(float (&v)[4], float* red, int& buf) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  auto fold = [&](float a0, float a1, float a2, float a3) -> float {   // lane's value index: bits 4 and 3
+    const bool up = lane & 16, hi = lane & 8;
+    const float b0 = (up ? a2 : a0) + __shfl_xor_sync(0xffffffffu, up ? a0 : a2, 16);
+    const float b1 = (up ? a3 : a1) + __shfl_xor_sync(0xffffffffu, up ? a1 : a3, 16);
+    float c = (hi ? b1 : b0) + __shfl_xor_sync(0xffffffffu, hi ? b0 : b1, 8);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+    for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    return c;
+  };
+  float c = fold(v[0], v[1], v[2], v[3]);
+  if (nw > 1) {
+    float* r = red + buf * (4 * 32);
+    buf ^= 1;
+    if ((lane & 7) == 0) r[(lane >> 3) * 32 + w] = c;   // value lane >> 3 of this warp
+    __syncthreads();
+    c = 0.0f;
+    for (int i = lane & 7; i < nw; i += 8) c += r[(lane >> 3) * 32 + i];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  const int nw = blockDim.x >> 5;
-  if (nw == 1) return;
-  float* r = red + buf * (3 * 32);
-  buf ^= 1;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0)
+    for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  }
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i * 32 + w] = v[i];
-  __syncthreads();
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, c, i * 8);
+}
+
+// Ring of rows: `stages` slots of ARRAYS x VPT vectors per thread. Every call
+// of fetch commits one group, so that a wait can count rows.
+template <int ARRAYS, int VPT>
+struct RowRing {
+  uint4* base;
+  int nt, nv, stages;
+  __device__ __forceinline__ const uint4* slot(int st) const { return base + (size_t)st * ARRAYS * VPT * nt; }
+  __device__ __forceinline__ void fetch(const uint4* const (&src)[ARRAYS], int row, bool on, int st) const {
+    if (on) {
+      uint4* to = base + (size_t)st * ARRAYS * VPT * nt;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < nw ? r[i * 32 + lane] : 0.0f;
+      for (int j = 0; j < VPT; ++j) {
+        const int v = (int)threadIdx.x + j * nt;
+        if (v < nv)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+          for (int a = 0; a < ARRAYS; ++a)
+            if (src[a]) cp_async16(to + (a * VPT + j) * nt, src[a] + (size_t)row * nv + v);
+      }
+    }
+    cp_async_commit();
+  }
+};
+
+// A thread's vectors of one row: zero where the row has none.
+template <int VPT>
+__device__ __forceinline__ uint4 row_vec(const uint4* slot, int array, int j, int nt, bool on) {
+  return on ? slot[(array * VPT + j) * nt] : make_uint4(0, 0, 0, 0);
 }
 
 template <typename T, int VPT>
-__global__ void __launch_bounds__(kNormMaxThreads) residual_norm_kernel(const NormParams p, int stages) {
+__global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const NormParams p, int stages) {
   constexpr int N = Vec16<T>::N;
-  extern __shared__ uint4 ring[];   // [stages][h, y][VPT][threads]
-  __shared__ float red[2 * 3 * 32];
+  extern __shared__ uint4 ring_mem[];
+  __shared__ float red[2 * 4 * 32];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.d / N;
   const bool has_y = p.y != nullptr, post = p.w_post != nullptr, pre = p.w_pre != nullptr;
-  const uint4* h = static_cast<const uint4*>(p.h);
-  const uint4* y = static_cast<const uint4*>(p.y);
+  const uint4* const src[2] = {static_cast<const uint4*>(p.h), static_cast<const uint4*>(p.y)};
+  const RowRing<2, VPT> ring = {ring_mem + tid, nt, nv, stages};
   uint4* h_out = static_cast<uint4*>(p.h_out);
   uint4* u = static_cast<uint4*>(p.u);
   const float inv_d = 1.0f / (float)p.d;
@@ -134,27 +170,32 @@ __global__ void __launch_bounds__(kNormMaxThreads) residual_norm_kernel(const No
     if (v < nv && pre) wpre[j] = __ldg(static_cast<const uint4*>(p.w_pre) + v);
   }
   int gate_row = -1;
-
-  auto fetch = [&](int t, int st) {
-    if (t < p.T) {
-      uint4* slot = ring + (size_t)st * 2 * VPT * nt + tid;
+  // Row k of this CTA: rows are dealt in turn, so that CTAs work on neighbours.
+  const int rows = p.T > (int)blockIdx.x ? (p.T - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  auto fetch = [&](int k, int st) { ring.fetch(src, blockIdx.x + k * gridDim.x, k < rows, st); };
+  auto sum_y = [&](const uint4* slot) -> float {     // this thread's share of y's squares
+    float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int v = tid + j * nt;
-        if (v < nv) {
-          cp_async16(slot + j * nt, h + (size_t)t * nv + v);
-          if (has_y) cp_async16(slot + (VPT + j) * nt, y + (size_t)t * nv + v);
-        }
-      }
+    for (int j = 0; j < VPT; ++j) {
+      float f[N];
+      unpack16<T>(row_vec<VPT>(slot, 1, j, nt, tid + j * nt < nv), f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) s = fmaf(f[i], f[i], s);
     }
-    cp_async_commit();
+    return s;
   };
-  // Rows are dealt in turn: consecutive CTAs work on neighbouring rows.
-  for (int i = 0; i < stages - 1; ++i) fetch(blockIdx.x + i * gridDim.x, i);
+  for (int k = 0; k < stages - 1; ++k) fetch(k, k);
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};             // y's squares of the row to come, the stream's
+  if (post && rows > 0) {
+    cp_async_wait(stages - 2);
+    s[0] = sum_y(ring.slot(0));
+    block_sum4(s, red, buf);
+  }
   int st = 0;
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const long long ahead = (long long)t + (long long)(stages - 1) * gridDim.x;
-    fetch(ahead < p.T ? (int)ahead : p.T, st == 0 ? stages - 1 : st - 1);
+  for (int k = 0; k < rows; ++k) {
+    const int t = blockIdx.x + k * gridDim.x;
+    const int next = st + 1 == stages ? 0 : st + 1;
+    fetch(k + stages - 1, st == 0 ? stages - 1 : st - 1);
     if (p.gate && t / p.gate_tokens != gate_row) {
       gate_row = t / p.gate_tokens;
 #pragma unroll
@@ -163,31 +204,16 @@ __global__ void __launch_bounds__(kNormMaxThreads) residual_norm_kernel(const No
           gate[j] = __ldg(static_cast<const uint4*>(p.gate) + (size_t)gate_row * nv + tid + j * nt);
     }
     cp_async_wait(stages - 1);
-    const uint4* slot = ring + (size_t)st * 2 * VPT * nt + tid;
-    if (++st == stages) st = 0;
-    float o[VPT][N], s[1] = {0.0f};
-    uint4 yv[VPT];
-    if (has_y) {
+    const uint4* slot = ring.slot(st);
+    float o[VPT][N], sh = 0.0f;
+    const float ry = post ? p.beta * rsqrtf(s[0] * inv_d + p.eps) : p.beta;
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) yv[j] = tid + j * nt < nv ? slot[(VPT + j) * nt] : make_uint4(0, 0, 0, 0);
-      float ry = p.beta;
-      if (post) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          float f[N];
-          unpack16<T>(yv[j], f);
-#pragma unroll
-          for (int i = 0; i < N; ++i) s[0] = fmaf(f[i], f[i], s[0]);
-        }
-        block_sum(s, red, buf);
-        ry *= rsqrtf(s[0] * inv_d + p.eps);
-        s[0] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
+    for (int j = 0; j < VPT; ++j) {
+      const bool on = tid + j * nt < nv;
+      unpack16<T>(row_vec<VPT>(slot, 0, j, nt, on), o[j]);
+      if (has_y) {
         float f[N], w[N], g[N];
-        unpack16<T>(tid + j * nt < nv ? slot[j * nt] : make_uint4(0, 0, 0, 0), o[j]);
-        unpack16<T>(yv[j], f);
+        unpack16<T>(row_vec<VPT>(slot, 1, j, nt, on), f);
         unpack16<T>(wpost[j], w);
         unpack16<T>(gate[j], g);
 #pragma unroll
@@ -196,23 +222,21 @@ __global__ void __launch_bounds__(kNormMaxThreads) residual_norm_kernel(const No
           if (post) b *= w[i] + p.w_offset;
           if (p.gate) b *= g[i];
           o[j][i] = fmaf(p.alpha, o[j][i], b);
-          s[0] = fmaf(o[j][i], o[j][i], s[0]);
         }
-        if (tid + j * nt < nv) h_out[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
+        if (on) h_out[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
       }
-    } else {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        unpack16<T>(tid + j * nt < nv ? slot[j * nt] : make_uint4(0, 0, 0, 0), o[j]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[0] = fmaf(o[j][i], o[j][i], s[0]);
-      }
+      for (int i = 0; i < N; ++i) sh = fmaf(o[j][i], o[j][i], sh);
     }
+    const bool more = post && k + 1 < rows;
+    if (more) cp_async_wait(stages - 2);
+    s[0] = more ? sum_y(ring.slot(next)) : 0.0f;
+    s[1] = sh;
+    if (pre || more) block_sum4(s, red, buf);
     if (pre) {
       // The norm reads the stream in fp32, before the rounding that h_out
       // takes: u is rounded once.
-      block_sum(s, red, buf);
-      const float r = rsqrtf(s[0] * inv_d + p.eps);
+      const float r = rsqrtf(s[1] * inv_d + p.eps);
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         float w[N];
@@ -222,110 +246,124 @@ __global__ void __launch_bounds__(kNormMaxThreads) residual_norm_kernel(const No
         if (tid + j * nt < nv) u[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
       }
     }
+    st = next;
   }
 }
 
 // Per run c: sums[0][c] dw_post, sums[1][c] dw_pre, sums[2][c] / sums[3][c]
-// the head and tail slots of the gate's gradient, each [d] fp32.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(kNormMaxThreads, 1)
+// the head and tail slots of the gate's gradient, each [d] fp32. PIPE: the
+// ring holds two rows at least, and a row's first sums are taken with the last
+// of the row before; else (rows past 28 KB) they have a barrier of their own.
+template <typename T, int VPT, bool PIPE>
+__global__ void __launch_bounds__(kNormBwdThreads, 1)
     residual_norm_bwd_kernel(const NormBwdParams p, int stages, int rows_per_run) {
   constexpr int N = Vec16<T>::N;
-  extern __shared__ uint4 ring[];   // [stages][h_out, y, du, dh_out][VPT][threads]
-  __shared__ float red[2 * 3 * 32];
+  extern __shared__ uint4 ring_mem[];
+  __shared__ float red[2 * 4 * 32];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int nv = p.d / N;
   const bool has_y = p.y != nullptr, post = p.w_post != nullptr, pre = p.w_pre != nullptr;
-  const uint4* src[4] = {static_cast<const uint4*>(p.h_out), static_cast<const uint4*>(p.y),
-                         static_cast<const uint4*>(p.du), static_cast<const uint4*>(p.dh_out)};
+  const uint4* const src[4] = {static_cast<const uint4*>(p.h_out), static_cast<const uint4*>(p.y),
+                               static_cast<const uint4*>(p.du), static_cast<const uint4*>(p.dh_out)};
+  const RowRing<4, VPT> ring = {ring_mem + tid, nt, nv, stages};
   const float inv_d = 1.0f / (float)p.d;
   int buf = 0;
   const int t0 = blockIdx.x * rows_per_run, t1 = min(p.T, t0 + rows_per_run);
   const int gt = p.gate ? p.gate_tokens : p.T;   // without a gate: one group
 
-  uint4 wpost[VPT], wpre[VPT], gate[VPT];
+  // In fp32: the pre norm's weights, and beta g (w_post + offset) of the gate row.
+  float wpre[VPT][N], wbr[VPT][N];
   float acc_post[VPT][N], acc_pre[VPT][N], acc_s[VPT][N];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = tid + j * nt;
-    wpost[j] = wpre[j] = gate[j] = make_uint4(0, 0, 0, 0);
-    if (v < nv && post) wpost[j] = __ldg(static_cast<const uint4*>(p.w_post) + v);
-    if (v < nv && pre) wpre[j] = __ldg(static_cast<const uint4*>(p.w_pre) + v);
+    unpack16<T>(v < nv && pre ? __ldg(static_cast<const uint4*>(p.w_pre) + v) : make_uint4(0, 0, 0, 0), wpre[j]);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc_post[j][i] = acc_pre[j][i] = acc_s[j][i] = 0.0f;
+    for (int i = 0; i < N; ++i) {
+      wpre[j][i] += p.w_offset;
+      acc_post[j][i] = acc_pre[j][i] = acc_s[j][i] = 0.0f;
+    }
   }
-  auto load_gate = [&](int row) {
-    if (!p.gate) return;
+  // Gate row and branch weight (1 without) of a vector, from L2.
+  auto gate_vec = [&](int row, int v, float (&g)[N], float (&w)[N]) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (tid + j * nt < nv) gate[j] = __ldg(static_cast<const uint4*>(p.gate) + (size_t)row * nv + tid + j * nt);
+    for (int i = 0; i < N; ++i) g[i] = w[i] = 1.0f;
+    if (p.gate) unpack16<T>(__ldg(static_cast<const uint4*>(p.gate) + (size_t)row * nv + v), g);
+    if (post) {
+      unpack16<T>(__ldg(static_cast<const uint4*>(p.w_post) + v), w);
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] += p.w_offset;
+    }
   };
-  auto fetch = [&](int t, int st) {
-    if (t < t1) {
-      uint4* slot = ring + (size_t)st * 4 * VPT * nt + tid;
+  auto open_gate = [&](int row) {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int v = tid + j * nt;
-        if (v < nv) {
+    for (int j = 0; j < VPT; ++j) {
+      float g[N], w[N];
+      gate_vec(row, min(tid + j * nt, nv - 1), g, w);
 #pragma unroll
-          for (int a = 0; a < 4; ++a)
-            if (src[a]) cp_async16(slot + (a * VPT + j) * nt, src[a] + (size_t)t * nv + v);
+      for (int i = 0; i < N; ++i) wbr[j][i] = p.beta * g[i] * w[i];
+    }
+  };
+  auto fetch = [&](int t, int st) { ring.fetch(src, t, t < t1, st); };
+  // This thread's shares of the sums of h'^2, q h', y^2.
+  auto first_sums = [&](const uint4* slot, float (&s)[4]) {
+    s[0] = s[1] = s[2] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const bool on = tid + j * nt < nv;
+      float f[N], q[N];
+      if (pre) {
+        unpack16<T>(row_vec<VPT>(slot, 0, j, nt, on), f);
+        unpack16<T>(row_vec<VPT>(slot, 2, j, nt, on), q);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          s[0] = fmaf(f[i], f[i], s[0]);
+          s[1] = fmaf(q[i] * wpre[j][i], f[i], s[1]);
         }
       }
+      if (post) {
+        unpack16<T>(row_vec<VPT>(slot, 1, j, nt, on), f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[2] = fmaf(f[i], f[i], s[2]);
+      }
     }
-    cp_async_commit();
   };
+
   for (int i = 0; i < stages - 1; ++i) fetch(t0 + i, i);
-  if (t0 < t1) load_gate(t0 / gt);
+  if (t0 < t1 && has_y) open_gate(t0 / gt);
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (PIPE && t0 < t1) {
+    cp_async_wait(stages - 2);
+    first_sums(ring.slot(0), s);
+    block_sum4(s, red, buf);
+  }
   int st = 0;
   for (int t = t0; t < t1; ++t) {
     fetch(t + stages - 1 < t1 ? t + stages - 1 : t1, st == 0 ? stages - 1 : st - 1);
     cp_async_wait(stages - 1);
-    const uint4* slot = ring + (size_t)st * 4 * VPT * nt + tid;
-    if (++st == stages) st = 0;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    // sums of h'^2, q h', y^2
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    if (pre || post) {
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        if (tid + j * nt >= nv) continue;
-        float f[N], q[N], w[N];
-        if (pre) {
-          unpack16<T>(slot[j * nt], f);
-          unpack16<T>(slot[(2 * VPT + j) * nt], q);
-          unpack16<T>(wpre[j], w);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            s[0] = fmaf(f[i], f[i], s[0]);
-            s[1] = fmaf(q[i] * (w[i] + p.w_offset), f[i], s[1]);
-          }
-        }
-        if (post) {
-          unpack16<T>(slot[(VPT + j) * nt], f);
-#pragma unroll
-          for (int i = 0; i < N; ++i) s[2] = fmaf(f[i], f[i], s[2]);
-        }
-      }
-      block_sum(s, red, buf);
+    const uint4* slot = ring.slot(st);
+    const int next = st + 1 == stages ? 0 : st + 1;
+    if (!PIPE) {
+      first_sums(slot, s);
+      s[3] = 0.0f;
+      block_sum4(s, red, buf);
     }
     const float rh = rsqrtf(s[0] * inv_d + p.eps), ry = post ? rsqrtf(s[2] * inv_d + p.eps) : 1.0f;
     const float ch = rh * rh * rh * s[1] * inv_d;
-    float dm[VPT][N], sy[1] = {0.0f};
+    float dm[VPT][N], sy = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const bool on = tid + j * nt < nv;
-      float dH[N], f[N], w[N], g[N];
-      unpack16<T>(on && src[3] ? slot[(3 * VPT + j) * nt] : zero, dH);
+      float dH[N], f[N];
+      unpack16<T>(row_vec<VPT>(slot, 3, j, nt, on && src[3]), dH);
       if (pre) {
         float q[N];
-        unpack16<T>(on ? slot[j * nt] : zero, f);
-        unpack16<T>(on ? slot[(2 * VPT + j) * nt] : zero, q);
-        unpack16<T>(wpre[j], w);
+        unpack16<T>(row_vec<VPT>(slot, 0, j, nt, on), f);
+        unpack16<T>(row_vec<VPT>(slot, 2, j, nt, on), q);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           acc_pre[j][i] = fmaf(q[i], f[i] * rh, acc_pre[j][i]);
-          dH[i] += rh * (q[i] * (w[i] + p.w_offset)) - ch * f[i];
+          dH[i] += rh * (q[i] * wpre[j][i]) - ch * f[i];
         }
       }
       if (p.dh && on) {
@@ -335,34 +373,34 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
         static_cast<uint4*>(p.dh)[(size_t)t * nv + tid + j * nt] = pack16<T>(a);
       }
       if (has_y) {
-        unpack16<T>(on ? slot[(VPT + j) * nt] : zero, f);
-        unpack16<T>(wpost[j], w);
-        unpack16<T>(gate[j], g);
+        unpack16<T>(row_vec<VPT>(slot, 1, j, nt, on), f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           acc_s[j][i] = fmaf(dH[i], f[i] * ry, acc_s[j][i]);
-          float b = p.beta * dH[i];
-          if (post) b *= w[i] + p.w_offset;
-          if (p.gate) b *= g[i];
-          dm[j][i] = b;
-          sy[0] = fmaf(b, f[i], sy[0]);
+          dm[j][i] = dH[i] * wbr[j][i];
+          sy = fmaf(dm[j][i], f[i], sy);
         }
       }
     }
+    const bool ahead = PIPE && t + 1 < t1;
+    if (ahead) {
+      cp_async_wait(stages - 2);
+      first_sums(ring.slot(next), s);
+    }
+    s[3] = sy;
+    if (ahead || post) block_sum4(s, red, buf);
     if (has_y) {
-      float cy = 0.0f;
-      if (post) {
-        block_sum(sy, red, buf);
-        cy = ry * ry * ry * sy[0] * inv_d;
-      }
+      const float cy = post ? ry * ry * ry * s[3] * inv_d : 0.0f;
+      if (p.dy) {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        if (tid + j * nt >= nv) continue;
-        float f[N], o[N];
-        unpack16<T>(slot[(VPT + j) * nt], f);
+        for (int j = 0; j < VPT; ++j) {
+          if (tid + j * nt >= nv) continue;
+          float f[N], o[N];
+          unpack16<T>(row_vec<VPT>(slot, 1, j, nt, true), f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = ry * dm[j][i] - cy * f[i];
-        if (p.dy) static_cast<uint4*>(p.dy)[(size_t)t * nv + tid + j * nt] = pack16<T>(o);
+          for (int i = 0; i < N; ++i) o[i] = ry * dm[j][i] - cy * f[i];
+          static_cast<uint4*>(p.dy)[(size_t)t * nv + tid + j * nt] = pack16<T>(o);
+        }
       }
       // The last row of its gate row, or of the run.
       const int grp = t / gt;
@@ -375,13 +413,12 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
         for (int j = 0; j < VPT; ++j) {
           if (tid + j * nt >= nv) continue;
           float w[N], g[N], o[N];
-          unpack16<T>(wpost[j], w);
-          unpack16<T>(gate[j], g);
+          gate_vec(grp, tid + j * nt, g, w);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const float b = p.beta * acc_s[j][i];
-            acc_post[j][i] = fmaf(b, p.gate ? g[i] : 1.0f, acc_post[j][i]);
-            o[i] = post ? b * (w[i] + p.w_offset) : b;
+            acc_post[j][i] = fmaf(b, g[i], acc_post[j][i]);
+            o[i] = b * w[i];
             acc_s[j][i] = 0.0f;
           }
           if (p.dgate) {
@@ -395,9 +432,10 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
             }
           }
         }
-        if (t + 1 < t1) load_gate(grp + 1);
+        if (t + 1 < t1) open_gate(grp + 1);
       }
     }
+    st = next;
   }
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -415,11 +453,13 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   }
 }
 
-// Adds the runs' sums in run order. blockIdx.y = 0: dw_post, 1: dw_pre, 2 + c:
-// the gate row that begins in run c and goes on past its end. 32 columns by
+// Adds the runs' sums in run order. blockIdx.y = 0: dw_post, 1: dw_pre, from 2
+// on: a gate row that straddles runs, by its own number, or (`by_run`, where
+// there are fewer runs than gate rows) by the run it begins in. 32 columns by
 // 16 slices of the runs per block.
 template <typename T>
-__global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p, int runs, int rows_per_run) {
+__global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p, int runs, int rows_per_run,
+                                                          int by_run) {
   __shared__ float part[16][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   const int what = blockIdx.y;
@@ -435,16 +475,18 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p,
     out = static_cast<T*>(p.dw_pre);
     base = p.partial + (size_t)runs * p.d;
     n = runs;
-  } else if (p.dgate) {
-    const int c = what - 2;
-    const long long t0 = (long long)c * rows_per_run, t1 = t0 + rows_per_run;   // t1 < T: c is not the last run
-    const long long grp = (t1 - 1) / p.gate_tokens;
-    if (t1 >= p.T || t1 / p.gate_tokens != grp || grp * p.gate_tokens < t0) return;
-    const long long end = min((grp + 1) * (long long)p.gate_tokens, (long long)p.T);
+  } else {
+    // The gate row of the last token of a run is the only one that can begin
+    // in it and go on.
+    const long long gt = p.gate_tokens;
+    const long long grp = by_run ? ((what - 2 + 1LL) * rows_per_run - 1) / gt : what - 2;
+    const long long begin = grp * gt, end = min(begin + gt, (long long)p.T);
+    const int c = (int)(begin / rows_per_run), last = (int)((end - 1) / rows_per_run);
+    if (last == c || (by_run && c != what - 2)) return;
     out = static_cast<T*>(p.dgate) + (size_t)grp * p.d;
     first = p.partial + ((size_t)3 * runs + c) * p.d;
     base = p.partial + ((size_t)2 * runs + c + 1) * p.d;
-    n = (int)((end - 1) / rows_per_run) - c;
+    n = last - c;
   }
   if (!out) return;
   const int per = ceil_div(n, 16);
@@ -467,16 +509,19 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p,
 struct NormShape {
   int vpt, threads, ctas_per_sm, stages, smem;
 };
-// A thread takes one 16-byte vector of a row, or two where 1024 threads do not
-// cover it; CTAs per SM fill about 1024 threads, and share 200 KB of ring.
-NormShape norm_shape(int dtype, int d, int arrays) {
+// Two 16-byte vectors a thread (one where 32 threads cover a row, four where
+// 512 do not with two); CTAs fill `per_sm` threads an SM and share 200 KB of
+// ring.
+NormShape norm_shape(int dtype, int d, int arrays, int per_sm) {
   const int nv = d / (dtype == MOE_DTYPE_F32 ? 4 : 8);
   NormShape s;
-  s.vpt = nv > kNormMaxThreads ? 2 : 1;
+  s.vpt = nv > 2 * 512 ? 4 : nv > 32 ? 2 : 1;
   s.threads = ceil_div(ceil_div(nv, s.vpt), 32) * 32;
-  s.ctas_per_sm = kNormMaxThreads / s.threads;
+  s.ctas_per_sm = per_sm / s.threads;
   if (s.ctas_per_sm > 16) s.ctas_per_sm = 16;
+  if (s.ctas_per_sm < 1) s.ctas_per_sm = 1;
   const int row = arrays * s.vpt * s.threads * 16;
+  if (200 * 1024 / s.ctas_per_sm / row < 2) s.ctas_per_sm = 1;
   s.stages = 200 * 1024 / s.ctas_per_sm / row;
   if (s.stages > kNormMaxStages) s.stages = kNormMaxStages;
   if (s.stages < 1) s.stages = 1;
@@ -493,17 +538,17 @@ cudaError_t allow_smem(K kernel, int smem) {
 }  // namespace
 
 bool norm_width_supported(int dtype, int d) {
-  return (long long)d * (dtype == MOE_DTYPE_F32 ? 4 : 2) <= 2 * kNormMaxThreads * 16;
+  return (long long)d * (dtype == MOE_DTYPE_F32 ? 4 : 2) <= 4 * kNormMaxThreads * 16;
 }
 
 int norm_backward_runs(int dtype, int T, int d, int num_sms) {
-  const long long n = (long long)norm_shape(dtype, d, 4).ctas_per_sm * num_sms;
+  const long long n = (long long)norm_shape(dtype, d, 4, 512).ctas_per_sm * num_sms;
   const int per = ceil_div(T, (int)(n < T ? n : T));
   return ceil_div(T, per);
 }
 
 cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.dtype, p.d, 2);
+  const NormShape sh = norm_shape(p.dtype, p.d, 2, 1024);
   const long long slots = (long long)sh.ctas_per_sm * num_sms;
   const int grid = (int)(slots < p.T ? slots : p.T);
   auto go = [&](auto kernel) {
@@ -512,13 +557,17 @@ cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t 
     kernel<<<grid, sh.threads, sh.smem, s>>>(p, sh.stages);
     return cudaGetLastError();
   };
-  if (p.dtype == MOE_DTYPE_F32)
-    return sh.vpt == 1 ? go(residual_norm_kernel<float, 1>) : go(residual_norm_kernel<float, 2>);
-  return sh.vpt == 1 ? go(residual_norm_kernel<__nv_bfloat16, 1>) : go(residual_norm_kernel<__nv_bfloat16, 2>);
+  auto with = [&](auto zero) {
+    using T = decltype(zero);
+    return sh.vpt == 1   ? go(residual_norm_kernel<T, 1>)
+           : sh.vpt == 2 ? go(residual_norm_kernel<T, 2>)
+                         : go(residual_norm_kernel<T, 4>);
+  };
+  return p.dtype == MOE_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
 }
 
 cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.dtype, p.d, 4);
+  const NormShape sh = norm_shape(p.dtype, p.d, 4, 512);
   const int runs = norm_backward_runs(p.dtype, p.T, p.d, num_sms);
   const int per = ceil_div(p.T, runs);
   auto go = [&](auto kernel) {
@@ -527,16 +576,22 @@ cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, c
     kernel<<<runs, sh.threads, sh.smem, s>>>(p, sh.stages, per);
     return cudaGetLastError();
   };
-  cudaError_t e;
-  if (p.dtype == MOE_DTYPE_F32)
-    e = sh.vpt == 1 ? go(residual_norm_bwd_kernel<float, 1>) : go(residual_norm_bwd_kernel<float, 2>);
-  else
-    e = sh.vpt == 1 ? go(residual_norm_bwd_kernel<__nv_bfloat16, 1>) : go(residual_norm_bwd_kernel<__nv_bfloat16, 2>);
+  auto with = [&](auto zero) {
+    using T = decltype(zero);
+    return sh.vpt == 1       ? go(residual_norm_bwd_kernel<T, 1, true>)
+           : sh.vpt == 2     ? go(residual_norm_bwd_kernel<T, 2, true>)
+           : sh.stages >= 2  ? go(residual_norm_bwd_kernel<T, 4, true>)
+                             : go(residual_norm_bwd_kernel<T, 4, false>);
+  };
+  const cudaError_t e = p.dtype == MOE_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
   if (e != cudaSuccess || !(p.dw_post || p.dw_pre || p.dgate)) return e;
-  const dim3 grid(ceil_div(p.d, 32), 2 + (p.dgate ? runs - 1 : 0));
+  // No gate row straddles runs of whole gate rows.
+  const int gates = ceil_div(p.T, p.gate_tokens < p.T ? p.gate_tokens : p.T), by_run = gates > runs - 1;
+  const int straddle = !p.dgate || per % p.gate_tokens == 0 ? 0 : by_run ? runs - 1 : gates;
+  const dim3 grid(ceil_div(p.d, 32), 2 + straddle);
   const dim3 block(32, 16);
-  if (p.dtype == MOE_DTYPE_F32) norm_reduce_kernel<float><<<grid, block, 0, s>>>(p, runs, per);
-  else norm_reduce_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(p, runs, per);
+  if (p.dtype == MOE_DTYPE_F32) norm_reduce_kernel<float><<<grid, block, 0, s>>>(p, runs, per, by_run);
+  else norm_reduce_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(p, runs, per, by_run);
   return cudaGetLastError();
 }
 

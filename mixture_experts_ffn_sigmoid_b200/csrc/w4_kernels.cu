@@ -306,13 +306,17 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
         for (int i = 0; i < 4; ++i) acc[a][t][i] = 0.0f;
     const int nch = ceil_div(sg.K, W4_CHUNK);
     for (int c = wk; c < nch; c += WK) {
-      uint32_t sc[2][HELD], zp[2][HELD];
+      uint32_t sc[2][HELD];                          // rows g and g + 8
+      float off[2][HELD][2];                         // with zero points: -scale (128 + zero), exact
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int e = 0; e < HELD; ++e) {
           sc[a][e] = (uint32_t)sc_r[a][0][e] | ((uint32_t)sc_r[a][1][e] << 16);
-          zp[a][e] = (uint32_t)z_r[a][0][e] | ((uint32_t)z_r[a][1][e] << 16);
+          if (p.has_zero)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              off[a][e][h] = __uint_as_float((uint32_t)sc_r[a][h][e] << 16) * (-128.0f - (float)(z_r[a][h][e] & 15));
         }
       issue(slot ^ 1);
       const bool whole = (c + 1) * W4_CHUNK <= sg.K;
@@ -366,20 +370,19 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
           if ((s + 1) % PER == 0) {                  // the group's sum is whole: its scale, from the lane that has it
             const int sub = s / PER;
             const uint32_t ss = __shfl_sync(0xffffffffu, sc[a][sub % HELD], (lane & 28) | (sub / HELD));
-            float z0 = -136.0f, z1 = -136.0f;
-            if (p.has_zero) {
-              const uint32_t zz = __shfl_sync(0xffffffffu, zp[a][sub % HELD], (lane & 28) | (sub / HELD));
-              z0 = -128.0f - (float)(zz & 15u);
-              z1 = -128.0f - (float)((zz >> 16) & 15u);
-            }
             const float s0 = __uint_as_float(ss << 16), s1 = __uint_as_float(ss & 0xffff0000u);
+            float o0 = -136.0f * s0, o1 = -136.0f * s1;
+            if (p.has_zero) {
+              o0 = __shfl_sync(0xffffffffu, off[a][sub % HELD][0], (lane & 28) | (sub / HELD));
+              o1 = __shfl_sync(0xffffffffu, off[a][sub % HELD][1], (lane & 28) | (sub / HELD));
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               if (t > 0 && t * 8 >= sg.rows) break;
-              acc[a][t][0] = fmaf(s0, fmaf(z0, xs[t][0], grp[a][t][0]), acc[a][t][0]);
-              acc[a][t][1] = fmaf(s0, fmaf(z0, xs[t][1], grp[a][t][1]), acc[a][t][1]);
-              acc[a][t][2] = fmaf(s1, fmaf(z1, xs[t][0], grp[a][t][2]), acc[a][t][2]);
-              acc[a][t][3] = fmaf(s1, fmaf(z1, xs[t][1], grp[a][t][3]), acc[a][t][3]);
+              acc[a][t][0] = fmaf(s0, grp[a][t][0], fmaf(o0, xs[t][0], acc[a][t][0]));
+              acc[a][t][1] = fmaf(s0, grp[a][t][1], fmaf(o0, xs[t][1], acc[a][t][1]));
+              acc[a][t][2] = fmaf(s1, grp[a][t][2], fmaf(o1, xs[t][0], acc[a][t][2]));
+              acc[a][t][3] = fmaf(s1, grp[a][t][3], fmaf(o1, xs[t][1], acc[a][t][3]));
             }
           }
         }
