@@ -40,8 +40,10 @@
 namespace moe {
 namespace {
 
-constexpr int kNormMaxThreads = 512;    // forward: two 16-byte vectors a thread, four past 16 KB rows
-constexpr int kNormBwdThreads = 512;
+// Two 16-byte vectors a thread up to 14 KB rows, then five: 448 threads leave
+// 73 registers each to two CTAs an SM, 146 to one.
+constexpr int kNormMaxThreads = 448;
+constexpr int kNormWideVpt = 5;
 constexpr int kNormMaxStages = 4;
 
 template <typename T> __device__ __forceinline__ void unpack16(const uint4& v, float (&f)[Vec16<T>::N]);
@@ -117,13 +119,27 @@ __device__ __forceinline__ void block_sum4(float (&v)[4], float* red, int& buf) 
   for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, c, i * 8);
 }
 
-// Ring of rows: `stages` slots of ARRAYS x VPT vectors per thread. Every call
-// of fetch commits one group, so that a wait can count rows.
+// Ring of rows: `stages` slots of ARRAYS x VPT vectors per thread. Vectors past
+// the row's end and arrays that are absent stay zero from the start, so that
+// readers need no case of their own. Every call of fetch commits one group, so
+// that a wait can count rows.
 template <int ARRAYS, int VPT>
 struct RowRing {
   uint4* base;
   int nt, nv, stages;
   __device__ __forceinline__ const uint4* slot(int st) const { return base + (size_t)st * ARRAYS * VPT * nt; }
+  __device__ __forceinline__ uint4 get(const uint4* slot, int array, int j) const {
+    return slot[(array * VPT + j) * nt];
+  }
+  __device__ __forceinline__ void clear(const uint4* const (&src)[ARRAYS]) const {
+    for (int st = 0; st < stages; ++st)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int a = 0; a < ARRAYS; ++a)
+          if (!src[a] || (int)threadIdx.x + j * nt >= nv)
+            base[((size_t)st * ARRAYS * VPT + a * VPT + j) * nt] = make_uint4(0, 0, 0, 0);
+  }
   __device__ __forceinline__ void fetch(const uint4* const (&src)[ARRAYS], int row, bool on, int st) const {
     if (on) {
       uint4* to = base + (size_t)st * ARRAYS * VPT * nt;
@@ -140,11 +156,42 @@ struct RowRing {
   }
 };
 
-// A thread's vectors of one row: zero where the row has none.
-template <int VPT>
-__device__ __forceinline__ uint4 row_vec(const uint4* slot, int array, int j, int nt, bool on) {
-  return on ? slot[(array * VPT + j) * nt] : make_uint4(0, 0, 0, 0);
-}
+// The branch's factor per column, beta g (w_post + offset), 1 for what is
+// absent. The gate row comes in ahead (packed), w_post from the caches.
+template <typename T, int VPT>
+struct BranchWeight {
+  static constexpr int N = Vec16<T>::N;
+  const uint4* gate;        // or null
+  const uint4* w_post;      // or null
+  float beta, w_offset;
+  int nt, nv;
+  uint4 next[VPT];
+  __device__ __forceinline__ int col(int j) const { return min((int)threadIdx.x + j * nt, nv - 1); }
+  __device__ __forceinline__ void load(int row) {
+    if (!gate) return;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) next[j] = __ldg(gate + (size_t)row * nv + col(j));
+  }
+  __device__ __forceinline__ void post_weights(int j, float (&w)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 1.0f;
+    if (w_post) {
+      unpack16<T>(__ldg(w_post + col(j)), w);
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] += w_offset;
+    }
+  }
+  __device__ __forceinline__ void open(float (&out)[VPT][N]) const {   // of the row loaded last
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float w[N], g[N];
+      post_weights(j, w);
+      if (gate) unpack16<T>(next[j], g);
+#pragma unroll
+      for (int i = 0; i < N; ++i) out[j][i] = beta * w[i] * (gate ? g[i] : 1.0f);
+    }
+  }
+};
 
 template <typename T, int VPT>
 __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const NormParams p, int stages) {
@@ -161,30 +208,34 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
   const float inv_d = 1.0f / (float)p.d;
   int buf = 0;
 
-  uint4 wpost[VPT], wpre[VPT], gate[VPT];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int v = tid + j * nt;
-    wpost[j] = wpre[j] = gate[j] = make_uint4(0, 0, 0, 0);
-    if (v < nv && post) wpost[j] = __ldg(static_cast<const uint4*>(p.w_post) + v);
-    if (v < nv && pre) wpre[j] = __ldg(static_cast<const uint4*>(p.w_pre) + v);
-  }
-  int gate_row = -1;
   // Row k of this CTA: rows are dealt in turn, so that CTAs work on neighbours.
   const int rows = p.T > (int)blockIdx.x ? (p.T - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-  auto fetch = [&](int k, int st) { ring.fetch(src, blockIdx.x + k * gridDim.x, k < rows, st); };
+  auto row_of = [&](int k) { return (int)blockIdx.x + k * (int)gridDim.x; };
+  auto fetch = [&](int k, int st) { ring.fetch(src, row_of(k), k < rows, st); };
+  ring.clear(src);
+  for (int k = 0; k < stages - 1; ++k) fetch(k, k);
+
+  uint4 wpre[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    wpre[j] = pre ? __ldg(static_cast<const uint4*>(p.w_pre) + min(tid + j * nt, nv - 1)) : make_uint4(0, 0, 0, 0);
+  BranchWeight<T, VPT> branch = {static_cast<const uint4*>(p.gate), static_cast<const uint4*>(p.w_post), p.beta,
+                                 p.w_offset, nt, nv};
+  float wbr[VPT][N];
+  int gate_row = rows > 0 ? row_of(0) / p.gate_tokens : 0;
+  branch.load(rows > 0 ? gate_row : 0);
+  branch.open(wbr);
   auto sum_y = [&](const uint4* slot) -> float {     // this thread's share of y's squares
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       float f[N];
-      unpack16<T>(row_vec<VPT>(slot, 1, j, nt, tid + j * nt < nv), f);
+      unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
       for (int i = 0; i < N; ++i) s = fmaf(f[i], f[i], s);
     }
     return s;
   };
-  for (int k = 0; k < stages - 1; ++k) fetch(k, k);
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};             // y's squares of the row to come, the stream's
   if (post && rows > 0) {
     cp_async_wait(stages - 2);
@@ -193,58 +244,50 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
   }
   int st = 0;
   for (int k = 0; k < rows; ++k) {
-    const int t = blockIdx.x + k * gridDim.x;
+    const int t = row_of(k);
     const int next = st + 1 == stages ? 0 : st + 1;
     fetch(k + stages - 1, st == 0 ? stages - 1 : st - 1);
-    if (p.gate && t / p.gate_tokens != gate_row) {
-      gate_row = t / p.gate_tokens;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j)
-        if (tid + j * nt < nv)
-          gate[j] = __ldg(static_cast<const uint4*>(p.gate) + (size_t)gate_row * nv + tid + j * nt);
-    }
     cp_async_wait(stages - 1);
     const uint4* slot = ring.slot(st);
     float o[VPT][N], sh = 0.0f;
-    const float ry = post ? p.beta * rsqrtf(s[0] * inv_d + p.eps) : p.beta;
+    const float ry = post ? rsqrtf(s[0] * inv_d + p.eps) : 1.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const bool on = tid + j * nt < nv;
-      unpack16<T>(row_vec<VPT>(slot, 0, j, nt, on), o[j]);
-      if (has_y) {
-        float f[N], w[N], g[N];
-        unpack16<T>(row_vec<VPT>(slot, 1, j, nt, on), f);
-        unpack16<T>(wpost[j], w);
-        unpack16<T>(gate[j], g);
+      float f[N];
+      unpack16<T>(ring.get(slot, 0, j), o[j]);
+      unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          float b = f[i] * ry;
-          if (post) b *= w[i] + p.w_offset;
-          if (p.gate) b *= g[i];
-          o[j][i] = fmaf(p.alpha, o[j][i], b);
-        }
-        if (on) h_out[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
+      for (int i = 0; i < N; ++i) {
+        o[j][i] = fmaf(ry, f[i] * wbr[j][i], p.alpha * o[j][i]);
+        sh = fmaf(o[j][i], o[j][i], sh);
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) sh = fmaf(o[j][i], o[j][i], sh);
+      if (has_y && tid + j * nt < nv) h_out[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
     }
-    const bool more = post && k + 1 < rows;
-    if (more) cp_async_wait(stages - 2);
-    s[0] = more ? sum_y(ring.slot(next)) : 0.0f;
+    const bool more = k + 1 < rows;
+    const int next_gate = more ? row_of(k + 1) / p.gate_tokens : gate_row;
+    if (next_gate != gate_row) branch.load(next_gate);
+    if (more && post) {
+      cp_async_wait(stages - 2);
+      s[0] = sum_y(ring.slot(next));
+    }
     s[1] = sh;
-    if (pre || more) block_sum4(s, red, buf);
+    if (pre || (more && post)) block_sum4(s, red, buf);
     if (pre) {
       // The norm reads the stream in fp32, before the rounding that h_out
       // takes: u is rounded once.
-      const float r = rsqrtf(s[1] * inv_d + p.eps);
+      const float r = rsqrtf(s[1] * inv_d + p.eps), ro = r * p.w_offset;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         float w[N];
         unpack16<T>(wpre[j], w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[j][i] *= r * (w[i] + p.w_offset);
+        for (int i = 0; i < N; ++i) o[j][i] *= fmaf(r, w[i], ro);
         if (tid + j * nt < nv) u[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
       }
+    }
+    if (next_gate != gate_row) {
+      gate_row = next_gate;
+      branch.open(wbr);
     }
     st = next;
   }
@@ -253,9 +296,9 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
 // Per run c: sums[0][c] dw_post, sums[1][c] dw_pre, sums[2][c] / sums[3][c]
 // the head and tail slots of the gate's gradient, each [d] fp32. PIPE: the
 // ring holds two rows at least, and a row's first sums are taken with the last
-// of the row before; else (rows past 28 KB) they have a barrier of their own.
+// of the row before; else (rows past 25 KB) they have a barrier of their own.
 template <typename T, int VPT, bool PIPE>
-__global__ void __launch_bounds__(kNormBwdThreads, 1)
+__global__ void __launch_bounds__(kNormMaxThreads, 1)
     residual_norm_bwd_kernel(const NormBwdParams p, int stages, int rows_per_run) {
   constexpr int N = Vec16<T>::N;
   extern __shared__ uint4 ring_mem[];
@@ -270,67 +313,47 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
   int buf = 0;
   const int t0 = blockIdx.x * rows_per_run, t1 = min(p.T, t0 + rows_per_run);
   const int gt = p.gate ? p.gate_tokens : p.T;   // without a gate: one group
+  auto fetch = [&](int t, int st) { ring.fetch(src, t, t < t1, st); };
+  ring.clear(src);
+  for (int i = 0; i < stages - 1; ++i) fetch(t0 + i, i);
 
-  // In fp32: the pre norm's weights, and beta g (w_post + offset) of the gate row.
-  float wpre[VPT][N], wbr[VPT][N];
+  float wpre[VPT][N], wbr[VPT][N];               // fp32, offsets and beta in
   float acc_post[VPT][N], acc_pre[VPT][N], acc_s[VPT][N];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    const int v = tid + j * nt;
-    unpack16<T>(v < nv && pre ? __ldg(static_cast<const uint4*>(p.w_pre) + v) : make_uint4(0, 0, 0, 0), wpre[j]);
+    unpack16<T>(pre ? __ldg(static_cast<const uint4*>(p.w_pre) + min(tid + j * nt, nv - 1)) : make_uint4(0, 0, 0, 0),
+                wpre[j]);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       wpre[j][i] += p.w_offset;
       acc_post[j][i] = acc_pre[j][i] = acc_s[j][i] = 0.0f;
     }
   }
-  // Gate row and branch weight (1 without) of a vector, from L2.
-  auto gate_vec = [&](int row, int v, float (&g)[N], float (&w)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) g[i] = w[i] = 1.0f;
-    if (p.gate) unpack16<T>(__ldg(static_cast<const uint4*>(p.gate) + (size_t)row * nv + v), g);
-    if (post) {
-      unpack16<T>(__ldg(static_cast<const uint4*>(p.w_post) + v), w);
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i] += p.w_offset;
-    }
-  };
-  auto open_gate = [&](int row) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      float g[N], w[N];
-      gate_vec(row, min(tid + j * nt, nv - 1), g, w);
-#pragma unroll
-      for (int i = 0; i < N; ++i) wbr[j][i] = p.beta * g[i] * w[i];
-    }
-  };
-  auto fetch = [&](int t, int st) { ring.fetch(src, t, t < t1, st); };
+  BranchWeight<T, VPT> branch = {static_cast<const uint4*>(p.gate), static_cast<const uint4*>(p.w_post), p.beta,
+                                 p.w_offset, nt, nv};
+  if (t0 < t1) {
+    branch.load(t0 / gt);
+    branch.open(wbr);
+  }
   // This thread's shares of the sums of h'^2, q h', y^2.
   auto first_sums = [&](const uint4* slot, float (&s)[4]) {
     s[0] = s[1] = s[2] = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const bool on = tid + j * nt < nv;
       float f[N], q[N];
-      if (pre) {
-        unpack16<T>(row_vec<VPT>(slot, 0, j, nt, on), f);
-        unpack16<T>(row_vec<VPT>(slot, 2, j, nt, on), q);
+      unpack16<T>(ring.get(slot, 0, j), f);
+      unpack16<T>(ring.get(slot, 2, j), q);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          s[0] = fmaf(f[i], f[i], s[0]);
-          s[1] = fmaf(q[i] * wpre[j][i], f[i], s[1]);
-        }
+      for (int i = 0; i < N; ++i) {
+        s[0] = fmaf(f[i], f[i], s[0]);
+        s[1] = fmaf(q[i] * wpre[j][i], f[i], s[1]);
       }
-      if (post) {
-        unpack16<T>(row_vec<VPT>(slot, 1, j, nt, on), f);
+      unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[2] = fmaf(f[i], f[i], s[2]);
-      }
+      for (int i = 0; i < N; ++i) s[2] = fmaf(f[i], f[i], s[2]);
     }
   };
 
-  for (int i = 0; i < stages - 1; ++i) fetch(t0 + i, i);
-  if (t0 < t1 && has_y) open_gate(t0 / gt);
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (PIPE && t0 < t1) {
     cp_async_wait(stages - 2);
@@ -348,40 +371,39 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
       s[3] = 0.0f;
       block_sum4(s, red, buf);
     }
-    const float rh = rsqrtf(s[0] * inv_d + p.eps), ry = post ? rsqrtf(s[2] * inv_d + p.eps) : 1.0f;
+    const float rh = pre ? rsqrtf(s[0] * inv_d + p.eps) : 0.0f, ry = post ? rsqrtf(s[2] * inv_d + p.eps) : 1.0f;
     const float ch = rh * rh * rh * s[1] * inv_d;
     float dm[VPT][N], sy = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const bool on = tid + j * nt < nv;
-      float dH[N], f[N];
-      unpack16<T>(row_vec<VPT>(slot, 3, j, nt, on && src[3]), dH);
-      if (pre) {
-        float q[N];
-        unpack16<T>(row_vec<VPT>(slot, 0, j, nt, on), f);
-        unpack16<T>(row_vec<VPT>(slot, 2, j, nt, on), q);
+      float dH[N], f[N], q[N];
+      unpack16<T>(ring.get(slot, 3, j), dH);
+      unpack16<T>(ring.get(slot, 0, j), f);
+      unpack16<T>(ring.get(slot, 2, j), q);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          acc_pre[j][i] = fmaf(q[i], f[i] * rh, acc_pre[j][i]);
-          dH[i] += rh * (q[i] * wpre[j][i]) - ch * f[i];
-        }
+      for (int i = 0; i < N; ++i) {
+        const float qr = q[i] * rh;
+        acc_pre[j][i] = fmaf(qr, f[i], acc_pre[j][i]);
+        dH[i] = fmaf(-ch, f[i], fmaf(qr, wpre[j][i], dH[i]));
       }
-      if (p.dh && on) {
+      if (p.dh && tid + j * nt < nv) {
         float a[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) a[i] = p.alpha * dH[i];
         static_cast<uint4*>(p.dh)[(size_t)t * nv + tid + j * nt] = pack16<T>(a);
       }
-      if (has_y) {
-        unpack16<T>(row_vec<VPT>(slot, 1, j, nt, on), f);
+      unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          acc_s[j][i] = fmaf(dH[i], f[i] * ry, acc_s[j][i]);
-          dm[j][i] = dH[i] * wbr[j][i];
-          sy = fmaf(dm[j][i], f[i], sy);
-        }
+      for (int i = 0; i < N; ++i) {
+        acc_s[j][i] = fmaf(dH[i], f[i] * ry, acc_s[j][i]);
+        dm[j][i] = dH[i] * wbr[j][i];
+        sy = fmaf(dm[j][i], f[i], sy);
       }
     }
+    // The last row of its gate row, or of the run: its sums go out below.
+    const int grp = t / gt;
+    const bool ends = (t + 1) % gt == 0 || t + 1 == p.T, close = ends || t + 1 == t1;
+    if (close && t + 1 < t1) branch.load(grp + 1);
     const bool ahead = PIPE && t + 1 < t1;
     if (ahead) {
       cp_async_wait(stages - 2);
@@ -389,51 +411,47 @@ __global__ void __launch_bounds__(kNormBwdThreads, 1)
     }
     s[3] = sy;
     if (ahead || post) block_sum4(s, red, buf);
-    if (has_y) {
+    if (p.dy) {
       const float cy = post ? ry * ry * ry * s[3] * inv_d : 0.0f;
-      if (p.dy) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          if (tid + j * nt >= nv) continue;
-          float f[N], o[N];
-          unpack16<T>(row_vec<VPT>(slot, 1, j, nt, true), f);
+      for (int j = 0; j < VPT; ++j) {
+        float f[N], o[N];
+        unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
-          for (int i = 0; i < N; ++i) o[i] = ry * dm[j][i] - cy * f[i];
-          static_cast<uint4*>(p.dy)[(size_t)t * nv + tid + j * nt] = pack16<T>(o);
-        }
+        for (int i = 0; i < N; ++i) o[i] = fmaf(ry, dm[j][i], -cy * f[i]);
+        if (tid + j * nt < nv) static_cast<uint4*>(p.dy)[(size_t)t * nv + tid + j * nt] = pack16<T>(o);
       }
-      // The last row of its gate row, or of the run.
-      const int grp = t / gt;
-      const bool ends = (t + 1) % gt == 0 || t + 1 == p.T;
-      if (ends || t + 1 == t1) {
-        const bool begins = (long long)grp * gt >= t0;
-        float* slot_f = nullptr;
-        if (!(begins && ends)) slot_f = p.partial + ((size_t)(begins ? 3 : 2) * gridDim.x + blockIdx.x) * p.d;
+    }
+    if (has_y && close) {
+      const bool begins = (long long)grp * gt >= t0;
+      float* slot_f = nullptr;
+      if (!(begins && ends)) slot_f = p.partial + ((size_t)(begins ? 3 : 2) * gridDim.x + blockIdx.x) * p.d;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          if (tid + j * nt >= nv) continue;
-          float w[N], g[N], o[N];
-          gate_vec(grp, tid + j * nt, g, w);
+      for (int j = 0; j < VPT; ++j) {
+        float w[N], g[N], o[N];
+        branch.post_weights(j, w);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float b = p.beta * acc_s[j][i];
-            acc_post[j][i] = fmaf(b, g[i], acc_post[j][i]);
-            o[i] = b * w[i];
-            acc_s[j][i] = 0.0f;
-          }
-          if (p.dgate) {
-            if (slot_f) {
+        for (int i = 0; i < N; ++i) g[i] = 1.0f;
+        if (p.gate) unpack16<T>(__ldg(static_cast<const uint4*>(p.gate) + (size_t)grp * nv + branch.col(j)), g);
 #pragma unroll
-              for (int i = 0; i < N; i += 4)
-                *reinterpret_cast<float4*>(slot_f + (size_t)(tid + j * nt) * N + i) =
-                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            } else {
-              static_cast<uint4*>(p.dgate)[(size_t)grp * nv + tid + j * nt] = pack16<T>(o);
-            }
+        for (int i = 0; i < N; ++i) {
+          const float b = p.beta * acc_s[j][i];
+          acc_post[j][i] = fmaf(b, g[i], acc_post[j][i]);
+          o[i] = b * w[i];
+          acc_s[j][i] = 0.0f;
+        }
+        if (p.dgate && tid + j * nt < nv) {
+          if (slot_f) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+              *reinterpret_cast<float4*>(slot_f + (size_t)(tid + j * nt) * N + i) =
+                  make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else {
+            static_cast<uint4*>(p.dgate)[(size_t)grp * nv + tid + j * nt] = pack16<T>(o);
           }
         }
-        if (t + 1 < t1) open_gate(grp + 1);
       }
+      if (t + 1 < t1) branch.open(wbr);
     }
     st = next;
   }
@@ -494,6 +512,7 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p,
   if (col < p.d) {
     if (first && threadIdx.y == 0) s = first[col];
     const int i1 = min(n, (int)(threadIdx.y + 1) * per);
+#pragma unroll 8
     for (int i = threadIdx.y * per; i < i1; ++i) s += base[(size_t)i * p.d + col];
   }
   part[threadIdx.y][threadIdx.x] = s;
@@ -509,13 +528,12 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p,
 struct NormShape {
   int vpt, threads, ctas_per_sm, stages, smem;
 };
-// Two 16-byte vectors a thread (one where 32 threads cover a row, four where
-// 512 do not with two); CTAs fill `per_sm` threads an SM and share 200 KB of
-// ring.
+// One 16-byte vector a thread where 32 threads cover a row, else two, else
+// five; CTAs fill `per_sm` threads an SM and share 200 KB of ring.
 NormShape norm_shape(int dtype, int d, int arrays, int per_sm) {
   const int nv = d / (dtype == MOE_DTYPE_F32 ? 4 : 8);
   NormShape s;
-  s.vpt = nv > 2 * 512 ? 4 : nv > 32 ? 2 : 1;
+  s.vpt = nv > 2 * kNormMaxThreads ? kNormWideVpt : nv > 32 ? 2 : 1;
   s.threads = ceil_div(ceil_div(nv, s.vpt), 32) * 32;
   s.ctas_per_sm = per_sm / s.threads;
   if (s.ctas_per_sm > 16) s.ctas_per_sm = 16;
@@ -538,17 +556,17 @@ cudaError_t allow_smem(K kernel, int smem) {
 }  // namespace
 
 bool norm_width_supported(int dtype, int d) {
-  return (long long)d * (dtype == MOE_DTYPE_F32 ? 4 : 2) <= 4 * kNormMaxThreads * 16;
+  return (long long)d * (dtype == MOE_DTYPE_F32 ? 4 : 2) <= 32768;
 }
 
 int norm_backward_runs(int dtype, int T, int d, int num_sms) {
-  const long long n = (long long)norm_shape(dtype, d, 4, 512).ctas_per_sm * num_sms;
+  const long long n = (long long)norm_shape(dtype, d, 4, kNormMaxThreads).ctas_per_sm * num_sms;
   const int per = ceil_div(T, (int)(n < T ? n : T));
   return ceil_div(T, per);
 }
 
 cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.dtype, p.d, 2, 1024);
+  const NormShape sh = norm_shape(p.dtype, p.d, 2, 2 * kNormMaxThreads);
   const long long slots = (long long)sh.ctas_per_sm * num_sms;
   const int grid = (int)(slots < p.T ? slots : p.T);
   auto go = [&](auto kernel) {
@@ -561,13 +579,13 @@ cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t 
     using T = decltype(zero);
     return sh.vpt == 1   ? go(residual_norm_kernel<T, 1>)
            : sh.vpt == 2 ? go(residual_norm_kernel<T, 2>)
-                         : go(residual_norm_kernel<T, 4>);
+                         : go(residual_norm_kernel<T, kNormWideVpt>);
   };
   return p.dtype == MOE_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
 }
 
 cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.dtype, p.d, 4, 512);
+  const NormShape sh = norm_shape(p.dtype, p.d, 4, kNormMaxThreads);
   const int runs = norm_backward_runs(p.dtype, p.T, p.d, num_sms);
   const int per = ceil_div(p.T, runs);
   auto go = [&](auto kernel) {
@@ -580,8 +598,8 @@ cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, c
     using T = decltype(zero);
     return sh.vpt == 1       ? go(residual_norm_bwd_kernel<T, 1, true>)
            : sh.vpt == 2     ? go(residual_norm_bwd_kernel<T, 2, true>)
-           : sh.stages >= 2  ? go(residual_norm_bwd_kernel<T, 4, true>)
-                             : go(residual_norm_bwd_kernel<T, 4, false>);
+           : sh.stages >= 2  ? go(residual_norm_bwd_kernel<T, kNormWideVpt, true>)
+                             : go(residual_norm_bwd_kernel<T, kNormWideVpt, false>);
   };
   const cudaError_t e = p.dtype == MOE_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
   if (e != cudaSuccess || !(p.dw_post || p.dw_pre || p.dgate)) return e;

@@ -525,12 +525,22 @@ template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16*
 // rounded to bf16 before the codes are taken: the
 // rounding costs no accuracy. A group of zeros gets scale 0; one that holds a
 // value that is not finite gets a NaN scale, so that it shows.
+//
+// round(w / scale) is taken from w times the reciprocal, which is off by less
+// than 1e-5 steps (two units of 2^-24 of at most 16); only where that lies
+// within 1e-4 of a half, and for scales whose reciprocal is not a normal
+// number, does the thread divide. 2^23 * 1.5 rounds to an integer in the
+// mantissa, ties to even. Dividing every weight took twice as long as the
+// kernel's bytes.
+constexpr float kRoundMagic = 12582912.0f;
+
 template <typename T>
-__global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ w, long long n8, int lanes,
+__global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ w, long long n8, int lanes_log2,
                                                           uint32_t* __restrict__ q, __nv_bfloat16* __restrict__ scale,
                                                           uint8_t* __restrict__ zero) {
   const long long stride = (long long)gridDim.x * blockDim.x;
   const long long start = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int lanes = 1 << lanes_log2;
   // Whole warps stay together over the shuffles: n8 is a multiple of `lanes`,
   // a group's lanes are in or out of range together.
   for (long long i = start; i - (threadIdx.x & 31) < n8; i += stride) {
@@ -540,33 +550,42 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ 
     else
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    float lo = 0.0f, hi = 0.0f;
-    int odd = 0;
+    float lo = 0.0f, hi = 0.0f, odd = 0.0f;            // odd: NaN once a value is not finite
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       lo = fminf(lo, f[j]);
       hi = fmaxf(hi, f[j]);
-      odd |= !isfinite(f[j]);
+      odd = fmaf(f[j], 0.0f, odd);
     }
     for (int o = 1; o < lanes; o <<= 1) {
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      odd |= __shfl_xor_sync(0xffffffffu, odd, o);
+      odd += __shfl_xor_sync(0xffffffffu, odd, o);
     }
     const __nv_bfloat16 s16 = __float2bfloat16_rn(zero ? (hi - lo) * (1.0f / 15.0f) : fmaxf(hi, -lo) * (1.0f / 7.0f));
-    const float s = __bfloat162float(s16), step = s > 0.0f ? s : 1.0f;
-    const float z = zero ? fminf(fmaxf(rintf(-lo / step), 0.0f), 15.0f) : 8.0f;
+    const float s = __bfloat162float(s16), step = s > 0.0f ? s : 1.0f, inv = 1.0f / step;
+    const int z = zero ? (int)fminf(fmaxf(rintf(-lo / step), 0.0f), 15.0f) : 8;
     uint32_t word = 0;
+    float far = 0.0f;                                  // the farthest from an integer
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float c = fminf(fmaxf(rintf(f[j] / step) + z, 0.0f), 15.0f);
+      const float t = f[j] * inv, m = t + kRoundMagic;
+      far = fmaxf(far, fabsf(t - (m - kRoundMagic)));
+      const int c = min(max(__float_as_int(m) - __float_as_int(kRoundMagic) + z, 0), 15);
       word |= (uint32_t)c << (4 * j);
+    }
+    if (!(far <= 0.4999f) || !(inv <= 1e37f)) {
+      word = 0;
+      for (int j = 0; j < 8; ++j) {
+        const float c = fminf(fmaxf(rintf(f[j] / step) + (float)z, 0.0f), 15.0f);
+        word |= (uint32_t)c << (4 * j);
+      }
     }
     if (on) {
       q[i] = word;
-      if (i % lanes == 0) {
-        scale[i / lanes] = odd ? __ushort_as_bfloat16(0x7fc0) : s16;
-        if (zero) zero[i / lanes] = (uint8_t)z;
+      if ((i & (lanes - 1)) == 0) {
+        scale[i >> lanes_log2] = odd == 0.0f ? s16 : __ushort_as_bfloat16(0x7fc0);
+        if (zero) zero[i >> lanes_log2] = (uint8_t)z;
       }
     }
   }
@@ -575,16 +594,18 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ 
 template <typename T>
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __restrict__ q,
                                                             const __nv_bfloat16* __restrict__ scale,
-                                                            const uint8_t* __restrict__ zero, long long n8, int lanes,
-                                                            T* __restrict__ w) {
+                                                            const uint8_t* __restrict__ zero, long long n8,
+                                                            int lanes_log2, T* __restrict__ w) {
   const long long stride = (long long)gridDim.x * blockDim.x;
+#pragma unroll 2
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += stride) {
     const uint32_t word = __ldg(q + i);
-    const float s = __bfloat162float(scale[i / lanes]);
-    const int z = zero ? (zero[i / lanes] & 15) : 8;
+    const float s = __bfloat162float(scale[i >> lanes_log2]);
+    // 2^23 + code is a float whose last bits are the code.
+    const float z = 8388608.0f + (float)(zero ? (zero[i >> lanes_log2] & 15) : 8);
     float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = s * (float)((int)((word >> (4 * j)) & 15u) - z);
+    for (int j = 0; j < 8; ++j) f[j] = s * (__uint_as_float(((word >> (4 * j)) & 15u) | 0x4b000000u) - z);
     store8(w + i * 8, f);
   }
 }
@@ -631,7 +652,7 @@ cudaError_t launch_w4_quantize(int dtype, const void* w, long long n, int group,
   const long long n8 = n / 8, blocks = ceil_div_ll(n8, 256);
   const int grid = (int)(blocks < 8LL * num_sms ? blocks : 8LL * num_sms);
   auto go = [&](auto kernel, auto* src) {
-    kernel<<<grid, 256, 0, s>>>(src, n8, group / 8, static_cast<uint32_t*>(q), static_cast<__nv_bfloat16*>(scale),
+    kernel<<<grid, 256, 0, s>>>(src, n8, group == 32 ? 2 : group == 64 ? 3 : 4, static_cast<uint32_t*>(q), static_cast<__nv_bfloat16*>(scale),
                                 static_cast<uint8_t*>(zero));
     return cudaGetLastError();
   };
@@ -645,7 +666,7 @@ cudaError_t launch_w4_dequantize(int dtype, const void* q, const void* scale, co
   const int grid = (int)(blocks < 8LL * num_sms ? blocks : 8LL * num_sms);
   auto go = [&](auto kernel, auto* dst) {
     kernel<<<grid, 256, 0, s>>>(static_cast<const uint32_t*>(q), static_cast<const __nv_bfloat16*>(scale),
-                                static_cast<const uint8_t*>(zero), n8, group / 8, dst);
+                                static_cast<const uint8_t*>(zero), n8, group == 32 ? 2 : group == 64 ? 3 : 4, dst);
     return cudaGetLastError();
   };
   if (dtype == MOE_DTYPE_F32) return go(w4_dequantize_kernel<float>, static_cast<float*>(w));
