@@ -246,6 +246,61 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _ptrs(*tensors):
+    """Device addresses (None for None) of contiguous CUDA tensors, all on the
+    current device: kernels are launched there, and another GPU's memory may
+    not be reachable from it."""
+    dev = None
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensor must live on a CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"tensor lives on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _args(*specs):
+    """Addresses of (tensor, name, least elements, dtype, required) in order.
+    One pass over tensors that are as they should be (a decode step makes many
+    small calls); anything else goes through _need and _ptrs for its error."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    out = []
+    for t, _, n, dt, required in specs:
+        if t is None:
+            if required and n > 0:
+                break
+            out.append(None)
+        elif isinstance(t, torch.Tensor) and t.dtype is dt and t.numel() >= n and t.get_device() == dev \
+                and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            break
+    else:
+        return out
+    for t, name, n, dt, required in specs:
+        if name == "workspace":
+            _need_ws(t)
+        else:
+            _need(t, name, n, dt, required)
+    return _ptrs(*(spec[0] for spec in specs))
+
+
+def _raw_stream(stream):
+    """The stream's handle; the current device's current stream for None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _check(status: int, where: str):
     if status != MOE_OK:
         raise MoEError(status, where)
@@ -563,8 +618,12 @@ class W4Matrix:
         moe_w4_quantize(w, m, stream)
         return m
 
-    def _c(self) -> CW4Matrix:
-        return CW4Matrix(*_ptrs(self.q, self.scale, self.zero))
+    def _c(self):
+        """Reference to the C struct, with the tensors' addresses of now."""
+        q, scale, zero = _args((self.q, "q", self.rows * (self.K // 2), _U8, True),
+                               (self.scale, "scale", self.rows * (self.K // self.group), torch.bfloat16, True),
+                               (self.zero, "zero", self.rows * (self.K // self.group), _U8, False))
+        return ctypes.byref(CW4Matrix(q, scale, zero))
 
 
 def _dense_code(w, name: str) -> int:
@@ -584,8 +643,8 @@ def moe_w4_quantize(w, out: W4Matrix, stream=None):
     code = _dense_code(w, "w")
     if w.numel() != out.rows * out.K:
         raise ValueError(f"w: {w.numel()} elements, out holds {out.rows * out.K}")
-    (pw,) = _ptrs(w)
-    _check(lib().moe_w4_quantize(out.rows, out.K, code, out.group, pw, ctypes.byref(out._c()), _stream(stream)),
+    (pw,) = _args((w, "w", 0, w.dtype, True))
+    _check(lib().moe_w4_quantize(out.rows, out.K, code, out.group, pw, out._c(), _raw_stream(stream)),
            "moe_w4_quantize")
 
 
@@ -594,8 +653,8 @@ def moe_w4_dequantize(m: W4Matrix, w, stream=None):
     code = _dense_code(w, "w")
     if w.numel() != m.rows * m.K:
         raise ValueError(f"w: {w.numel()} elements, m holds {m.rows * m.K}")
-    (pw,) = _ptrs(w)
-    _check(lib().moe_w4_dequantize(m.rows, m.K, code, m.group, ctypes.byref(m._c()), pw, _stream(stream)),
+    (pw,) = _args((w, "w", 0, w.dtype, True))
+    _check(lib().moe_w4_dequantize(m.rows, m.K, code, m.group, m._c(), pw, _raw_stream(stream)),
            "moe_w4_dequantize")
 
 
@@ -617,25 +676,22 @@ def _w4_args(c: CConfig, w1, w3, w2, ws1, ws3, ws2):
             raise ValueError(f"{name}: group {m.group}, the others have {group}")
         group = m.group
         out.append(m)
-    return group, [None if m is None else ctypes.byref(m._c()) for m in out]
+    return group, [None if m is None else m._c() for m in out]
 
 
 def moe_expert_swiglu_w4(cfg, x, perm_src, expert_offsets, w1, w3, w2, x_shared, ws1, ws3, ws2, y_perm, y_shared,
                          workspace, stream=None):
     """moe_expert_swiglu on 4-bit weights (W4Matrix); rows gathered from x by perm_src, or packed if it is None."""
     c = _cfg(cfg)
-    R, dt, sh = c.T * c.k, _dt(c), c.f_shared > 0
-    _need(x, "x", (R if perm_src is None else c.T) * c.d, dt)
-    _need(perm_src, "perm_src", R, _I32, required=False)
-    _need(expert_offsets, "expert_offsets", c.E + 1, _I32)
-    _need(x_shared, "x_shared", c.T * c.d, dt, required=sh)
-    _need(y_perm, "y_perm", R * c.d, dt)
-    _need(y_shared, "y_shared", c.T * c.d, dt, required=sh)
-    _need_ws(workspace)
+    R, d, dt, sh = c.T * c.k, c.d, _dt(c), c.f_shared > 0
+    px, pp, po, pxs, py, pys, pw = _args(
+        (x, "x", (R if perm_src is None else c.T) * d, dt, True), (perm_src, "perm_src", R, _I32, False),
+        (expert_offsets, "expert_offsets", c.E + 1, _I32, True), (x_shared, "x_shared", c.T * d, dt, sh),
+        (y_perm, "y_perm", R * d, dt, True), (y_shared, "y_shared", c.T * d, dt, sh),
+        (workspace, "workspace", 1, _U8, True))
     group, (a1, a3, a2, s1, s3, s2) = _w4_args(c, w1, w3, w2, ws1, ws3, ws2)
-    px, pp, po, pxs, py, pys, pw = _ptrs(x, perm_src, expert_offsets, x_shared, y_perm, y_shared, workspace)
     _check(lib().moe_expert_swiglu_w4(ctypes.byref(c), group, px, pp, po, a1, a3, a2, pxs, s1, s3, s2, py, pys, pw,
-                                      workspace.numel(), _stream(stream)), "moe_expert_swiglu_w4")
+                                      workspace.numel(), _raw_stream(stream)), "moe_expert_swiglu_w4")
 
 
 def moe_forward_w4(cfg, x, w_router, bias, w1, w3, w2, ws1, ws3, ws2, y, workspace, stream=None):
@@ -693,12 +749,10 @@ def moe_orthogonalize(cfg, g, o, workspace, coeffs=None, stream=None):
     """Newton-Schulz orthogonalisation of every matrix of g [n, rows, cols] into o (bf16)."""
     c = _ocfg(cfg)
     n = c.n * c.rows * c.cols
-    _need(g, "g", n, _dt(c))
-    _need(o, "o", n, torch.bfloat16)
-    _need_ws(workspace)
     abc = _coeffs(c, coeffs)
-    pg, po, pw = _ptrs(g, o, workspace)
-    _check(lib().moe_orthogonalize(ctypes.byref(c), abc, pg, po, pw, workspace.numel(), _stream(stream)),
+    pg, po, pw = _args((g, "g", n, _dt(c), True), (o, "o", n, torch.bfloat16, True),
+                       (workspace, "workspace", 1, _U8, True))
+    _check(lib().moe_orthogonalize(ctypes.byref(c), abc, pg, po, pw, workspace.numel(), _raw_stream(stream)),
            "moe_orthogonalize")
 
 
@@ -708,14 +762,11 @@ def moe_muon_step(cfg, g, momentum, weight, workspace, lr: float, mu: float = 0.
     c = _ocfg(cfg)
     n = c.n * c.rows * c.cols
     code = _dense_code(weight, "weight")
-    _need(g, "g", n, _dt(c))
-    _need(momentum, "momentum", n, _F32)
-    _need(weight, "weight", n, weight.dtype)
-    _need_ws(workspace)
     abc = _coeffs(c, coeffs)
-    pg, pm, pw, ps = _ptrs(g, momentum, weight, workspace)
+    pg, pm, pw, ps = _args((g, "g", n, _dt(c), True), (momentum, "momentum", n, _F32, True),
+                           (weight, "weight", n, weight.dtype, True), (workspace, "workspace", 1, _U8, True))
     _check(lib().moe_muon_step(ctypes.byref(c), abc, pg, pm, pw, code, lr, mu, int(nesterov), weight_decay, scale, ps,
-                               workspace.numel(), _stream(stream)), "moe_muon_step")
+                               workspace.numel(), _raw_stream(stream)), "moe_muon_step")
 
 
 # ------------------------------------------------------------ residual norms
@@ -736,47 +787,19 @@ def _ncfg(c) -> CNormConfig:
     return c if isinstance(c, CNormConfig) else make_norm_config(c)
 
 
-def _ptrs(*tensors):
-    """Device addresses (None for None) of contiguous CUDA tensors, all on the
-    current device: kernels are launched there, and another GPU's memory may
-    not be reachable from it."""
-    dev = None
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensor must live on a CUDA device")
-        if not t.is_contiguous():
-            raise ValueError("tensor must be contiguous")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"tensor lives on cuda:{t.get_device()}, the current device is cuda:{dev}")
-        out.append(t.data_ptr())
-    return out
-
-
-def _need_norm(c: CNormConfig, y, w_post, gate, w_pre):
-    dt, n = _dt(c), c.T * c.d
-    _need(y, "y", n, dt, required=False)
-    _need(w_post, "w_post", c.d, dt, required=False)
-    if gate is not None and c.gate_tokens >= 1:
-        _need(gate, "gate", -(-c.T // c.gate_tokens) * c.d, dt)
-    _need(w_pre, "w_pre", c.d, dt, required=False)
+def _gate_elems(c: CNormConfig) -> int:
+    return -(-c.T // max(c.gate_tokens, 1)) * c.d
 
 
 def moe_residual_norm(cfg, h, y, w_post, gate, w_pre, h_out, u, stream=None):
     """h_out = alpha h + beta gate . N(y; w_post) and u = N(h_out; w_pre) in one pass."""
     c = _ncfg(cfg)
-    dt, n = _dt(c), c.T * c.d
-    _need(h, "h", n, dt)
-    _need_norm(c, y, w_post, gate, w_pre)
-    _need(h_out, "h_out", n, dt, required=y is not None)
-    _need(u, "u", n, dt, required=w_pre is not None)
-    _check(lib().moe_residual_norm(ctypes.byref(c), *_ptrs(h, y, w_post, gate, w_pre, h_out, u), _stream(stream)),
-           "moe_residual_norm")
+    dt, d = _dt(c), c.d
+    n = c.T * d
+    a = _args((h, "h", n, dt, True), (y, "y", n, dt, False), (w_post, "w_post", d, dt, False),
+              (gate, "gate", _gate_elems(c), dt, False), (w_pre, "w_pre", d, dt, False),
+              (h_out, "h_out", n, dt, y is not None), (u, "u", n, dt, w_pre is not None))
+    _check(lib().moe_residual_norm(ctypes.byref(c), *a, _raw_stream(stream)), "moe_residual_norm")
 
 
 def norm_backward_workspace_size(cfg) -> int:
@@ -794,20 +817,15 @@ def moe_residual_norm_backward(cfg, h_out, y, w_post, gate, w_pre, du, dh_out, d
                                workspace, stream=None):
     """Gradients of moe_residual_norm, given those of u and of h_out (None: none)."""
     c = _ncfg(cfg)
-    dt, n = _dt(c), c.T * c.d
-    _need(h_out, "h_out", n, dt, required=w_pre is not None)
-    _need_norm(c, y, w_post, gate, w_pre)
-    _need(du, "du", n, dt, required=w_pre is not None)
-    for t, name in ((dh_out, "dh_out"), (dh, "dh"), (dy, "dy")):
-        _need(t, name, n, dt, required=False)
-    for t, name in ((dw_post, "dw_post"), (dw_pre, "dw_pre")):
-        _need(t, name, c.d, dt, required=False)
-    if dgate is not None and c.gate_tokens >= 1:
-        _need(dgate, "dgate", -(-c.T // c.gate_tokens) * c.d, dt)
-    _need_ws(workspace)
-    _check(lib().moe_residual_norm_backward(
-        ctypes.byref(c), *_ptrs(h_out, y, w_post, gate, w_pre, du, dh_out, dh, dy, dw_post, dgate, dw_pre, workspace),
-        workspace.numel(), _stream(stream)), "moe_residual_norm_backward")
+    dt, d, gates = _dt(c), c.d, _gate_elems(c)
+    n = c.T * d
+    a = _args((h_out, "h_out", n, dt, w_pre is not None), (y, "y", n, dt, False), (w_post, "w_post", d, dt, False),
+              (gate, "gate", gates, dt, False), (w_pre, "w_pre", d, dt, False),
+              (du, "du", n, dt, w_pre is not None), (dh_out, "dh_out", n, dt, False), (dh, "dh", n, dt, False),
+              (dy, "dy", n, dt, False), (dw_post, "dw_post", d, dt, False), (dgate, "dgate", gates, dt, False),
+              (dw_pre, "dw_pre", d, dt, False), (workspace, "workspace", 1, _U8, True))
+    _check(lib().moe_residual_norm_backward(ctypes.byref(c), *a, workspace.numel(), _raw_stream(stream)),
+           "moe_residual_norm_backward")
 
 
 def moe_get_device_error(workspace, stream=None) -> int:

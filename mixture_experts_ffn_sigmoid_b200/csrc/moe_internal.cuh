@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 
 namespace moe {
@@ -293,5 +295,19 @@ size_t ortho_workspace_bytes(int n_mat, int rows, int cols, int num_sms);
 cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cudaStream_t s);
 
 int device_sm_count();
+
+// Lets a kernel take all 227 KB of dynamic shared memory, once per device.
+template <auto Kernel> struct KernelTag { static constexpr auto value = Kernel; };
+template <auto Kernel> cudaError_t allow_max_smem() {
+  static std::atomic<uint64_t> done{0};   // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && ((done.load(std::memory_order_relaxed) >> dev) & 1))) return e;
+  cudaFuncAttributes at;
+  if ((e = cudaFuncGetAttributes(&at, Kernel)) != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - (int)at.sharedSizeBytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace moe

@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   const float inv_d = 1.0f / (float)p.d;
   int buf = 0;
   const int t0 = blockIdx.x * rows_per_run, t1 = min(p.T, t0 + rows_per_run);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the reduction may line up
   const int gt = p.gate ? p.gate_tokens : p.T;   // without a gate: one group
   auto fetch = [&](int t, int st) { ring.fetch(src, t, t < t1, st); };
   ring.clear(src);
@@ -473,14 +474,15 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
 
 // Adds the runs' sums in run order. blockIdx.y = 0: dw_post, 1: dw_pre, from 2
 // on: a gate row that straddles runs, by its own number, or (`by_run`, where
-// there are fewer runs than gate rows) by the run it begins in. 32 columns by
-// 16 slices of the runs per block.
+// there are fewer runs than gate rows) by the run it begins in. 128
+// columns, four a thread, by 16 slices of the runs per block.
 template <typename T>
 __global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p, int runs, int rows_per_run,
                                                           int by_run) {
-  __shared__ float part[16][33];
-  const int col = blockIdx.x * 32 + threadIdx.x;
+  __shared__ float4 part[16][32];
+  const int col = (blockIdx.x * 32 + threadIdx.x) * 4;    // d is a multiple of 4
   const int what = blockIdx.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the runs' sums
   T* out = nullptr;
   const float* first = nullptr;   // one row outside the sequence, added first
   const float* base = nullptr;
@@ -508,20 +510,26 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(const NormBwdParams p,
   }
   if (!out) return;
   const int per = ceil_div(n, 16);
-  float s = 0.0f;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](const float4 v) {
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  };
   if (col < p.d) {
-    if (first && threadIdx.y == 0) s = first[col];
+    if (first && threadIdx.y == 0) add(*reinterpret_cast<const float4*>(first + col));
     const int i1 = min(n, (int)(threadIdx.y + 1) * per);
 #pragma unroll 8
-    for (int i = threadIdx.y * per; i < i1; ++i) s += base[(size_t)i * p.d + col];
+    for (int i = threadIdx.y * per; i < i1; ++i) add(*reinterpret_cast<const float4*>(base + (size_t)i * p.d + col));
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && col < p.d) {
-    s = 0.0f;
+    s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += part[i][threadIdx.x];
-    out[col] = from_f32<T>(s);
+    for (int i = 0; i < 16; ++i) add(part[i][threadIdx.x]);
+    out[col] = from_f32<T>(s.x);
+    out[col + 1] = from_f32<T>(s.y);
+    out[col + 2] = from_f32<T>(s.z);
+    out[col + 3] = from_f32<T>(s.w);
   }
 }
 
@@ -547,12 +555,6 @@ NormShape norm_shape(int dtype, int d, int arrays, int per_sm) {
   return s;
 }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, int smem) {
-  if (smem <= 32 * 1024) return cudaSuccess;   // with the static arrays below the default 48 KB
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-}
-
 }  // namespace
 
 bool norm_width_supported(int dtype, int d) {
@@ -569,17 +571,18 @@ cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t 
   const NormShape sh = norm_shape(p.dtype, p.d, 2, 2 * kNormMaxThreads);
   const long long slots = (long long)sh.ctas_per_sm * num_sms;
   const int grid = (int)(slots < p.T ? slots : p.T);
-  auto go = [&](auto kernel) {
-    cudaError_t e = allow_smem(kernel, sh.smem);
+  auto go = [&](auto tag) {
+    constexpr auto kernel = decltype(tag)::value;
+    const cudaError_t e = allow_max_smem<kernel>();
     if (e != cudaSuccess) return e;
     kernel<<<grid, sh.threads, sh.smem, s>>>(p, sh.stages);
     return cudaGetLastError();
   };
   auto with = [&](auto zero) {
     using T = decltype(zero);
-    return sh.vpt == 1   ? go(residual_norm_kernel<T, 1>)
-           : sh.vpt == 2 ? go(residual_norm_kernel<T, 2>)
-                         : go(residual_norm_kernel<T, kNormWideVpt>);
+    return sh.vpt == 1   ? go(KernelTag<residual_norm_kernel<T, 1>>{})
+           : sh.vpt == 2 ? go(KernelTag<residual_norm_kernel<T, 2>>{})
+                         : go(KernelTag<residual_norm_kernel<T, kNormWideVpt>>{});
   };
   return p.dtype == MOE_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
 }
@@ -588,29 +591,36 @@ cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, c
   const NormShape sh = norm_shape(p.dtype, p.d, 4, kNormMaxThreads);
   const int runs = norm_backward_runs(p.dtype, p.T, p.d, num_sms);
   const int per = ceil_div(p.T, runs);
-  auto go = [&](auto kernel) {
-    cudaError_t e = allow_smem(kernel, sh.smem);
+  auto go = [&](auto tag) {
+    constexpr auto kernel = decltype(tag)::value;
+    const cudaError_t e = allow_max_smem<kernel>();
     if (e != cudaSuccess) return e;
     kernel<<<runs, sh.threads, sh.smem, s>>>(p, sh.stages, per);
     return cudaGetLastError();
   };
   auto with = [&](auto zero) {
     using T = decltype(zero);
-    return sh.vpt == 1       ? go(residual_norm_bwd_kernel<T, 1, true>)
-           : sh.vpt == 2     ? go(residual_norm_bwd_kernel<T, 2, true>)
-           : sh.stages >= 2  ? go(residual_norm_bwd_kernel<T, kNormWideVpt, true>)
-                             : go(residual_norm_bwd_kernel<T, kNormWideVpt, false>);
+    return sh.vpt == 1       ? go(KernelTag<residual_norm_bwd_kernel<T, 1, true>>{})
+           : sh.vpt == 2     ? go(KernelTag<residual_norm_bwd_kernel<T, 2, true>>{})
+           : sh.stages >= 2  ? go(KernelTag<residual_norm_bwd_kernel<T, kNormWideVpt, true>>{})
+                             : go(KernelTag<residual_norm_bwd_kernel<T, kNormWideVpt, false>>{});
   };
   const cudaError_t e = p.dtype == MOE_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
   if (e != cudaSuccess || !(p.dw_post || p.dw_pre || p.dgate)) return e;
   // No gate row straddles runs of whole gate rows.
   const int gates = ceil_div(p.T, p.gate_tokens < p.T ? p.gate_tokens : p.T), by_run = gates > runs - 1;
   const int straddle = !p.dgate || per % p.gate_tokens == 0 ? 0 : by_run ? runs - 1 : gates;
-  const dim3 grid(ceil_div(p.d, 32), 2 + straddle);
-  const dim3 block(32, 16);
-  if (p.dtype == MOE_DTYPE_F32) norm_reduce_kernel<float><<<grid, block, 0, s>>>(p, runs, per, by_run);
-  else norm_reduce_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(p, runs, per, by_run);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(p.d, 128), 2 + straddle);
+  cfg.blockDim = dim3(32, 16);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return p.dtype == MOE_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, norm_reduce_kernel<float>, p, runs, per, by_run)
+                                  : cudaLaunchKernelEx(&cfg, norm_reduce_kernel<__nv_bfloat16>, p, runs, per, by_run);
 }
 
 }  // namespace moe

@@ -34,8 +34,6 @@
 // stored once. The last step's epilogue writes the result or the weights.
 #include <cuda_fp16.h>
 
-#include <atomic>
-
 #include "umma_common.cuh"
 
 namespace moe {
@@ -555,15 +553,8 @@ bool make_ns_tmap(CUtensorMap* tm, const void* base, long long cols, long long r
 template <int MODE>
 cudaError_t launch_ns_gemm(const CUtensorMap& tp, const CUtensorMap& tq, const NsGemmParams& p, int num_sms,
                            cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};   // devices whose limit is raised, one bit each
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_max_smem<ns_gemm_kernel<MODE>>();
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !((done.load(std::memory_order_relaxed) >> dev) & 1)) {
-    e = cudaFuncSetAttribute(ns_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) done.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
-  }
   const long long tm = ceil_div(p.m, NS_TILE);
   const long long tiles = p.n_mat * (MODE == kNsGram || MODE == kNsPoly ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, NS_TILE));
   const int pairs = num_sms / 2;

@@ -522,19 +522,27 @@ template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16*
 
 // scale = (largest magnitude) * (1/7) with the codes centred on 8, or (max -
 // min) * (1/15) with a zero point, the factors and products in fp32; it is
-// rounded to bf16 before the codes are taken: the
-// rounding costs no accuracy. A group of zeros gets scale 0; one that holds a
-// value that is not finite gets a NaN scale, so that it shows.
+// rounded to bf16 before the codes are taken: the rounding costs no accuracy.
+// A group of zeros gets scale 0; one that holds a value that is not finite
+// gets a NaN scale, so that it shows (the extremes are taken so that a NaN
+// wins).
 //
 // round(w / scale) is taken from w times the reciprocal, which is off by less
-// than 1e-5 steps (two units of 2^-24 of at most 16); only where that lies
-// within 1e-4 of a half, and for scales whose reciprocal is not a normal
-// number, does the thread divide. 2^23 * 1.5 rounds to an integer in the
-// mantissa, ties to even. Dividing every weight took twice as long as the
-// kernel's bytes.
+// than 1e-5 steps (four units of 2^-24 of at most 16); only where that lies
+// within 1e-4 of a half, and for scales near the ends of fp32's range, does
+// the thread divide. Adding 2^23 * 1.5 rounds to an integer in the mantissa,
+// ties to even; 8 more is even and changes no tie. Dividing every weight took
+// three times as long as the kernel's bytes.
 constexpr float kRoundMagic = 12582912.0f;
+constexpr int W4_QUANT_AHEAD = 2;   // vectors a thread loads at once
 
-template <typename T>
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <typename T, bool ZERO>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ w, long long n8, int lanes_log2,
                                                           uint32_t* __restrict__ q, __nv_bfloat16* __restrict__ scale,
                                                           uint8_t* __restrict__ zero) {
@@ -543,49 +551,56 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ 
   const int lanes = 1 << lanes_log2;
   // Whole warps stay together over the shuffles: n8 is a multiple of `lanes`,
   // a group's lanes are in or out of range together.
-  for (long long i = start; i - (threadIdx.x & 31) < n8; i += stride) {
-    const bool on = i < n8;
-    float f[8];
-    if (on) load8(w + i * 8, f);
-    else
+  for (long long i0 = start; i0 - (threadIdx.x & 31) < n8; i0 += W4_QUANT_AHEAD * stride) {
+    float f[W4_QUANT_AHEAD][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    float lo = 0.0f, hi = 0.0f, odd = 0.0f;            // odd: NaN once a value is not finite
+    for (int k = 0; k < W4_QUANT_AHEAD; ++k) {
+      if (i0 + k * stride < n8) load8(w + (i0 + k * stride) * 8, f[k]);
+      else
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo = fminf(lo, f[j]);
-      hi = fmaxf(hi, f[j]);
-      odd = fmaf(f[j], 0.0f, odd);
+        for (int j = 0; j < 8; ++j) f[k][j] = 0.0f;
     }
-    for (int o = 1; o < lanes; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      odd += __shfl_xor_sync(0xffffffffu, odd, o);
-    }
-    const __nv_bfloat16 s16 = __float2bfloat16_rn(zero ? (hi - lo) * (1.0f / 15.0f) : fmaxf(hi, -lo) * (1.0f / 7.0f));
-    const float s = __bfloat162float(s16), step = s > 0.0f ? s : 1.0f, inv = 1.0f / step;
-    const int z = zero ? (int)fminf(fmaxf(rintf(-lo / step), 0.0f), 15.0f) : 8;
-    uint32_t word = 0;
-    float far = 0.0f;                                  // the farthest from an integer
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float t = f[j] * inv, m = t + kRoundMagic;
-      far = fmaxf(far, fabsf(t - (m - kRoundMagic)));
-      const int c = min(max(__float_as_int(m) - __float_as_int(kRoundMagic) + z, 0), 15);
-      word |= (uint32_t)c << (4 * j);
-    }
-    if (!(far <= 0.4999f) || !(inv <= 1e37f)) {
-      word = 0;
+    for (int k = 0; k < W4_QUANT_AHEAD; ++k) {
+      const long long i = i0 + k * stride;
+      float hi = 0.0f, neg = 0.0f;                     // largest value, or magnitude; largest of -w
+#pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float c = fminf(fmaxf(rintf(f[j] / step) + (float)z, 0.0f), 15.0f);
-        word |= (uint32_t)c << (4 * j);
+        hi = max_nan(hi, ZERO ? f[k][j] : fabsf(f[k][j]));
+        if (ZERO) neg = max_nan(neg, -f[k][j]);
       }
-    }
-    if (on) {
-      q[i] = word;
-      if ((i & (lanes - 1)) == 0) {
-        scale[i >> lanes_log2] = odd == 0.0f ? s16 : __ushort_as_bfloat16(0x7fc0);
-        if (zero) zero[i >> lanes_log2] = (uint8_t)z;
+      for (int o = 1; o < lanes; o <<= 1) {
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        if (ZERO) neg = max_nan(neg, __shfl_xor_sync(0xffffffffu, neg, o));
+      }
+      const bool finite = hi < INFINITY && neg < INFINITY;
+      const __nv_bfloat16 s16 = __float2bfloat16_rn(ZERO ? (hi + neg) * (1.0f / 15.0f) : hi * (1.0f / 7.0f));
+      const float s = __bfloat162float(s16), step = s > 0.0f ? s : 1.0f, inv = __fdividef(1.0f, step);
+      const int z = ZERO ? (int)fminf(fmaxf(rintf(neg / step), 0.0f), 15.0f) : 8;
+      uint32_t word = 0;
+      float far = 0.0f;                                // the farthest from an integer
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = f[k][j] * inv, m = t + kRoundMagic;
+        far = fmaxf(far, fabsf(t - (m - kRoundMagic)));
+        int c = __float_as_int(m) - __float_as_int(kRoundMagic) + z;
+        if (ZERO) c = min(max(c, 0), 15);              // without: |t| <= 7.03, 1 to 15 as it is
+        word |= (uint32_t)(c & 15) << (4 * j);
+      }
+      if (!(far <= 0.4999f) || !(step > 1e-37f && step < 1e37f)) {
+        word = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float c = fminf(fmaxf(rintf(f[k][j] / step) + (float)z, 0.0f), 15.0f);
+          word |= (uint32_t)c << (4 * j);
+        }
+      }
+      if (i < n8) {
+        q[i] = word;
+        if ((i & (lanes - 1)) == 0) {
+          scale[i >> lanes_log2] = finite ? s16 : __ushort_as_bfloat16(0x7fc0);
+          if (ZERO) zero[i >> lanes_log2] = (uint8_t)z;
+        }
       }
     }
   }
@@ -617,8 +632,9 @@ cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
   const int nt = w4_token_tiles(p);
   const int wk = w4_split(p, slots);
   const int n_seg = p.n_routed + (p.dense_rows > 0 ? 1 : 0);
-  auto go = [&](auto kernel, int smem) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto go = [&](auto tag, int smem) {
+    constexpr auto kernel = decltype(tag)::value;
+    const cudaError_t e = allow_max_smem<kernel>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(slots);
@@ -635,9 +651,9 @@ cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
   auto with = [&](auto mats, auto n) {
     constexpr int M = decltype(mats)::value, N = decltype(n)::value;
     const int smem = w4_smem_bytes<N>(n_seg);
-    return p.group == 128  ? go(w4_gemm_kernel<M, N, 128>, smem)
-           : p.group == 64 ? go(w4_gemm_kernel<M, N, 64>, smem)
-                           : go(w4_gemm_kernel<M, N, 32>, smem);
+    return p.group == 128  ? go(KernelTag<w4_gemm_kernel<M, N, 128>>{}, smem)
+           : p.group == 64 ? go(KernelTag<w4_gemm_kernel<M, N, 64>>{}, smem)
+                           : go(KernelTag<w4_gemm_kernel<M, N, 32>>{}, smem);
   };
   auto rows_of = [&](auto n) {
     return p.mats == 2 ? with(std::integral_constant<int, 2>{}, n) : with(std::integral_constant<int, 1>{}, n);
@@ -656,8 +672,12 @@ cudaError_t launch_w4_quantize(int dtype, const void* w, long long n, int group,
                                 static_cast<uint8_t*>(zero));
     return cudaGetLastError();
   };
-  if (dtype == MOE_DTYPE_F32) return go(w4_quantize_kernel<float>, static_cast<const float*>(w));
-  return go(w4_quantize_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16*>(w));
+  if (dtype == MOE_DTYPE_F32) {
+    const float* src = static_cast<const float*>(w);
+    return zero ? go(w4_quantize_kernel<float, true>, src) : go(w4_quantize_kernel<float, false>, src);
+  }
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w);
+  return zero ? go(w4_quantize_kernel<__nv_bfloat16, true>, src) : go(w4_quantize_kernel<__nv_bfloat16, false>, src);
 }
 
 cudaError_t launch_w4_dequantize(int dtype, const void* q, const void* scale, const void* zero, long long n, int group,
