@@ -521,8 +521,8 @@ typedef struct {
  *
  * moe_w4_dequantize - the dense values back, rounded to dtype once.
  *
- * Both: rows >= 0 (0 enqueues nothing), K a multiple of group; q, scale and w
- * 16-byte aligned, zero any. They serve any shape stack [..][K] with rows the
+ * Both: rows >= 0 (0 enqueues nothing), K a multiple of group; q, scale, zero
+ * and w 16-byte aligned. They serve any shape stack [..][K] with rows the
  * product of the leading sizes.
  */
 MOE_API moe_status moe_w4_quantize(int64_t rows, int32_t K, int32_t dtype, int32_t group, const void* w,
@@ -544,7 +544,7 @@ MOE_API moe_status moe_w4_dequantize(int64_t rows, int32_t K, int32_t dtype, int
  *                  (NULL if f_shared == 0)
  *   y_perm         [T*k][d] bf16 OUT, y_shared [T][d] bf16 OUT (NULL if f_shared == 0)
  *
- * bf16 rows only, d, f and f_shared multiples of group, else
+ * bf16 rows only, d, f and f_shared multiples of group and at most 16384, else
  * MOE_ERR_UNSUPPORTED. The SwiGLU intermediate is rounded to bf16 once, as in
  * moe_expert_swiglu. Any T is computed; the weights of an expert are read
  * again for every 8 to 32 of its rows, so long batches belong to

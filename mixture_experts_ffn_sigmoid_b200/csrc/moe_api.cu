@@ -797,11 +797,12 @@ moe_status check_ortho_ws(const moe_ortho_config& c, void* ws, size_t bytes) {
 // ---- 4-bit weights
 bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
 
-// A 4-bit matrix: q and scale 16-byte aligned, zero NULL or anywhere.
+// A 4-bit matrix: 16-byte aligned pointers, zero may be NULL.
 moe_status need_w4(const moe_w4_matrix* m) {
   if (!m) return MOE_ERR_INVALID_ARG;
   MOE_TRY(need(m->q));
-  return need(m->scale);
+  MOE_TRY(need(m->scale));
+  return m->zero ? need(m->zero) : MOE_OK;
 }
 W4Operand w4_operand(const moe_w4_matrix* m) {
   return {static_cast<const uint8_t*>(m->q), m->scale, static_cast<const uint8_t*>(m->zero)};
@@ -816,9 +817,11 @@ moe_status check_w4_matrix(int64_t rows, int K, int dtype, int group) {
 moe_status check_w4(const moe_config& c, int group) {
   if (!w4_group_ok(group)) return MOE_ERR_INVALID_ARG;
   if (c.dtype != MOE_DTYPE_BF16 || c.d % group || c.f % group || c.f_shared % group) return MOE_ERR_UNSUPPORTED;
-  // Work units (16 weight rows x 8 token rows) are counted in 32 bits.
-  const long long tiles = (c.d > c.f ? c.d : c.f) / 16, rows = (long long)c.T * (c.k + 1) / 8 + c.E + 1;
-  if (tiles * rows > 0x7fffffffLL || (long long)c.T * c.f_shared / 128 > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  // A token row and a unit's scales fit in shared memory.
+  if (c.d > 16384 || c.f > 16384 || c.f_shared > 16384) return MOE_ERR_UNSUPPORTED;
+  // Chunks (16 weight rows, 256 k, a pass over token rows) are counted in 32 bits.
+  const long long w = c.d > c.f ? (c.d > c.f_shared ? c.d : c.f_shared) : (c.f > c.f_shared ? c.f : c.f_shared);
+  if (((long long)c.T * (c.k + 1) + c.E + 1) * (w / 16) > 0x7fffffffLL / (w / 256 + 1)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -859,7 +862,9 @@ moe_status enqueue_experts_w4(const moe_config& c, int group, const void* x, con
     g.w_s[1] = w4_operand(ws3);
   }
   g.err = at<uint32_t>(ws, L.err);
+  g.check = 1;
   g.err_keep = err_keep;
+  g.timeout_ns = kDefaultTimeoutNs;
   g.has_zero = w1->zero || w3->zero || (shared && (ws1->zero || ws3->zero));
   MOE_CUDA(launch_w4_gemm(g, device_sm_count(), s));
   W4GemmParams q = {};
@@ -879,6 +884,8 @@ moe_status enqueue_experts_w4(const moe_config& c, int group, const void* x, con
     q.w_s[0] = w4_operand(ws2);
   }
   q.has_zero = w2->zero || (shared && ws2->zero);
+  q.err = g.err;
+  q.timeout_ns = g.timeout_ns;
   q.wait_previous = 1;
   MOE_CUDA(launch_w4_gemm(q, device_sm_count(), s));
   return MOE_OK;

@@ -269,7 +269,9 @@ struct W4GemmParams {
   const void* x_s; void* out_s;
   W4Operand w[2], w_s[2];
   int has_zero;             // some operand has zero points
-  uint32_t* err;            // or null: no check of offsets and gather
+  int check;                // check offsets and gather, and write the error word anew
+  uint32_t* err;
+  long long timeout_ns;
   int err_keep;             // add to the word what earlier kernels of the call left in it
   int wait_previous;        // start early, wait for the launch before (programmatic dependence)
 };

@@ -10,35 +10,42 @@
 // What bounds it: a decode batch gives an expert a handful of rows, so its
 // weights cross HBM for a few operations each. Four bits and a bf16 scale per
 // G make that 0.5 + 2/G bytes a weight (3/G with zero points), a quarter of
-// bf16. The products are small enough for the legacy tensor path: one
-// mma.sync m16n8k16 takes 16 weight rows x 8 tokens from registers, where the
-// codes are unpacked; tcgen05 would want the unpacked weights written back to
-// shared memory first, four times the bytes that HBM delivers.
+// bf16; unpacking them is what then fills the SM. The products are small
+// enough for the register-operand tensor path (tcgen05 would want unpacked
+// weights written back to shared memory first): one mma.sync m16n8k16 takes 16
+// weight rows x 8 tokens, with fp16 operands, because a code needs no
+// arithmetic to become one: the half 0x000c is the subnormal number c 2^-24,
+// exactly, and 0x00c0 is 16 times that. A 32-bit word holds eight codes of
+// consecutive k; it and itself shifted by 8, masked by 0x000f000f and
+// 0x00f000f0, are four operand pairs: five instructions per eight weights (the
+// 128 + code form of bf16 took seven and a subtraction, e4m3 operands twelve,
+// as their products run as fp16 ones on sm_100a).
 //
-// Unpacking: a 32-bit word holds eight codes c0..c7 of consecutive k. (w >> 4i)
-// & 0x000f000f is the pair (ci, c(i+4)); OR-ed with 0x4300 it is the pair of
-// bf16 numbers 128 + code. The products run over these, and the 128 + zero
-// that is too much comes off each group's sum in fp32, sum_k x_k of the group
-// being one more product with a matrix of ones (shared by every row): seven
-// integer instructions per eight weights and no arithmetic on them. The group's
-// fp32 sum then takes its scale. No weight is rounded; the sums run about 30
-// times as large as the result, which costs five of fp32's 24 bits and stays
-// far below the rounding of the bf16 output. The order of k inside a group is
-// free as long as both operands agree: token rows are paired the same way
-// (x_i, x_(i+4)), by byte permutes in gate/up; h is written in that order, so
-// the down product needs none.
+// Token rows as fp16: a row is scaled by the power of two that brings its
+// largest magnitude into [2^14, 2^15), the k under the 0x00f0 masks by 1/16
+// besides. fp16's eleven bits hold bf16's eight; only values below 2^-27 of
+// the row's largest lose bits. A CTA makes them in shared memory when it comes
+// to a segment, with each group's sum, off which the zero points come: it is
+// where the group's product starts from. The product takes its scale in fp32.
+// No weight is rounded.
 //
-// Layout of the work: a CTA of 8 warps takes a contiguous run of units; a unit
-// is 16 WM rows of W1 and W3 (32 WM rows of W2) of one expert times up to 8 NT
-// of its token rows, its K split over WK = 8 / WM warps in chunks of 256, two
-// 16-row tiles a warp, which share the token fragments. Each warp streams its
-// chunks through a ring of cp.async stages of its own, across unit boundaries,
-// so weights keep flowing while a unit's partial sums meet in shared memory.
-// Units of the non-empty segments only are dealt, evenly, so a batch that
-// touches few experts still uses every SM.
+// Layout of the work: the tiles of all non-empty segments (16 rows of W1 and W3,
+// or 32 rows of W2, with up to 8 NT of the segment's token rows) are dealt to
+// the CTAs in contiguous runs of equal length, so a batch that touches few
+// experts still uses every SM. Within a CTA a run is cut where the token rows
+// change; the chunks (256 k) of each piece's tiles go to the 8 warps in equal
+// contiguous shares. A tile that straddles warps is finished by the one that
+// began it, the others leave their sums in shared memory: no barrier but the
+// two around a piece. Each warp streams its chunks through a ring of its own,
+// its first lane starts a tile by one TMA (128 bytes by 16 rows, 128-byte
+// swizzle: the word reads then meet every bank once), across pieces, so weights
+// flow all the time. What is left to the lanes per 1024 weights (32 k of two
+// tiles) is 5 shared reads, 20 integer instructions and 4 products.
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
-#include "moe_internal.cuh"
+#include "umma_common.cuh"
 
 namespace moe {
 namespace {
@@ -48,67 +55,102 @@ constexpr int W4_THREADS = W4_WARPS * 32;
 constexpr int W4_CHUNK = 256;                       // k of one ring stage
 constexpr int W4_TILE_BYTES = 16 * W4_CHUNK / 2;    // 16 rows of codes
 constexpr int W4_STAGE_BYTES = 2 * W4_TILE_BYTES;
-constexpr int W4_STAGES = 2;
+constexpr int W4_MAX_STAGES = 3;
 
-__device__ __forceinline__ uint32_t w4_smem(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+// A bounded wait by a whole warp, with one outcome for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* err,
+                                          long long timeout_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err, timeout_ns, true));
 }
-// 16 bytes, or zeros where !valid (nothing is read then).
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// c = a b, and c += a b.
-__device__ __forceinline__ void mma_16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// c = i + a b, and c += a b, fp16 operands.
+__device__ __forceinline__ void mma_f16_from(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float i0,
+                                              float i1, float i2, float i3) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(i0), "f"(i1), "f"(i2), "f"(i3));
 }
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The four bf16 pairs (128 + ci, 128 + c(i+4)) of a word.
+// Two floats as a pair of fp16.
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The four operand pairs of a word of codes: (c0, c4), 16 (c1, c5), (c2, c6), 16 (c3, c7).
 __device__ __forceinline__ void unpack_w4(uint32_t w, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  p[0] = w & 0x000f000fu;
+  p[1] = w & 0x00f000f0u;
+  p[2] = (w >> 8) & 0x000f000fu;
+  p[3] = (w >> 8) & 0x00f000f0u;
 }
 
-struct W4Seg {   // one segment's share of a unit
-  const W4Operand* op;      // [MATS] matrices
-  size_t row0;              // first weight row of the segment in its matrix
-  int M, K;
-  int t0, rows;             // token rows [t0, t0 + rows) of the pass
-  bool dense;
-};
-
-// What a CTA knows of the i-th non-empty segment: x = units up to its end, y =
+// What a CTA knows of the i-th non-empty segment: x = chunks up to its end, y =
 // its expert (n_routed: the dense one), z = its first token row, w = its rows.
 using W4Entry = int4;
 
-// MATS = 2: gate/up, the two tiles of a warp are the same rows of W1 and W3.
-// MATS = 1: down, they are 16 rows of W2 and the 16 after them.
-template <int MATS, int NT, int GROUP>
-__global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmParams p, int WK) {
-  constexpr int RED = 2 * NT * 32;                        // float4s of one warp's partial sums
-  constexpr int WROWS = MATS == 2 ? 16 : 32;              // weight rows of a warp
-  extern __shared__ __align__(128) uint8_t w4_dyn[];
+// Shared memory of a CTA: rings | sums left by warps that did not begin a tile |
+// token rows in fp16 [rows][x_stride] | -8 or -1 times the groups' sums [K /
+// GROUP][8 NT] | the rows' factors [8 NT] | table.
+struct W4Plan {
+  int stages;
+  int rows;                 // token rows of a pass, at most 8 NT
+  int x_stride;             // bytes of a token row
+  int red, x, xs, f, tab;   // offsets
+};
+
+struct W4Piece {            // a run of one segment's tiles with the same token rows
+  const W4Operand* op;
+  size_t row0;              // first weight row of the segment in its matrix
+  int M, K, nch;            // chunks of a tile
+  int t0, rows;             // token rows [t0, t0 + rows)
+  int tile0, tiles;         // the run
+  bool dense;
+};
+
+template <int MATS, int NT, int GROUP, bool ZERO>
+__global__ void __launch_bounds__(W4_THREADS, 2)
+    w4_gemm_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
+                   const __grid_constant__ CUtensorMap tm0s, const __grid_constant__ CUtensorMap tm1s,
+                   const W4GemmParams p, const W4Plan plan) {
+  constexpr int RED = 2 * NT * 32;                        // float4s of one warp's sums
+  constexpr int WROWS = MATS == 2 ? 16 : 32;              // weight rows of a tile
+  constexpr int NG = W4_CHUNK / GROUP;                    // groups of a chunk: 2, 4 or 8
+  constexpr int PER = GROUP / 32;                         // steps of 32 k in a group
+  constexpr int HELD = NG > 4 ? 2 : 1;                    // scales of a row that a lane loads: 4 lanes share a row's
+  extern __shared__ uint8_t w4_raw[];
+  uint8_t* w4_dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w4_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int warp_n[W4_WARPS];
   __shared__ long long warp_u[W4_WARPS];
+  __shared__ uint64_t full_bar[W4_WARPS][W4_MAX_STAGES];
+  __shared__ uint32_t abort_word;
+  __shared__ int bad_word;
+  volatile uint32_t* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int WM = W4_WARPS / WK, wk = warp % WK, wm = warp / WK;
-  uint8_t* ring = w4_dyn + (size_t)warp * W4_STAGES * W4_STAGE_BYTES;
-  float4* red = reinterpret_cast<float4*>(w4_dyn + (size_t)W4_WARPS * W4_STAGES * W4_STAGE_BYTES);
-  W4Entry* tab = reinterpret_cast<W4Entry*>(red + W4_WARPS * RED);
+  const int stages = plan.stages;
+  const uint8_t* ring = w4_dyn + (size_t)warp * stages * W4_STAGE_BYTES;
+  float4* red = reinterpret_cast<float4*>(w4_dyn + plan.red);
+  uint8_t* xp = w4_dyn + plan.x;
+  float* xsum = reinterpret_cast<float*>(w4_dyn + plan.xs);
+  float2* xfac = reinterpret_cast<float2*>(w4_dyn + plan.f);
+  W4Entry* tab = reinterpret_cast<W4Entry*>(w4_dyn + plan.tab);
+  if (tid == 0) {
+    for (int w = 0; w < W4_WARPS; ++w)
+      for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full_bar[w][i]), 1);
+    abort_word = 0u;
+    bad_word = 0;
+    fence_mbar_init();
+    tmap_prefetch(&tm0);
+    if (MATS == 2) tmap_prefetch(&tm1);
+  }
 
   // -------------------------------------------------- the segments' table
   const int n_seg = p.n_routed + (p.dense_rows > 0 ? 1 : 0);
-  const int unit_rows = WROWS * WM;
   int base_n = 0;
   long long base_u = 0;
   for (int s0 = 0; s0 < n_seg; s0 += W4_THREADS) {
@@ -116,15 +158,16 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
     int begin = 0, rows = 0;
     long long units = 0;
     if (s < n_seg) {
-      int M = p.M_s;
+      int M = p.M_s, K = p.K_s;
       if (s < p.n_routed) {
         M = p.M;
+        K = p.K;
         begin = min(max(p.offsets[s], 0), p.max_rows);
         rows = min(max(p.offsets[s + 1], 0), p.max_rows) - begin;   // below 0 (a bad table): no rows
       } else {
         rows = p.dense_rows;
       }
-      if (rows > 0) units = (long long)ceil_div(M, unit_rows) * ceil_div(rows, 8 * NT);
+      if (rows > 0) units = (long long)ceil_div(M, WROWS) * ceil_div(K, W4_CHUNK) * ceil_div(rows, plan.rows);
     }
     const unsigned act = __ballot_sync(0xffffffffu, units > 0);
     long long inc = units;
@@ -157,286 +200,383 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_gemm_kernel(const W4GemmPara
   // A count past 32 bits comes from overlapping segments, a bad table: no work.
   const int n_act = base_n, total = base_u <= 0x7fffffffLL ? (int)base_u : 0;
   if (!p.wait_previous) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int u0 = (int)((long long)total * blockIdx.x / gridDim.x);
-  const int u1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
 
-  // Unit -> segment, tile of weight rows, pass over its token rows. Passes run
-  // innermost: the weights they share are still in L2.
-  auto locate = [&](int u, int& hint, W4Seg& sg, int& m0) {
-    while (u >= tab[hint].x) ++hint;
-    const W4Entry e = tab[hint];
-    const int s = e.y, begin = e.z, rows = e.w, passes = ceil_div(rows, 8 * NT);
-    const int rel = u - (hint ? tab[hint - 1].x : 0);
-    sg.dense = s >= p.n_routed;
-    sg.op = sg.dense ? p.w_s : p.w;
-    sg.M = sg.dense ? p.M_s : p.M;
-    sg.K = sg.dense ? p.K_s : p.K;
-    sg.row0 = sg.dense ? 0 : (size_t)s * p.M;
-    const int pass = rel % passes;
-    sg.t0 = begin + pass * 8 * NT;
-    sg.rows = min(8 * NT, rows - pass * 8 * NT);
-    m0 = (rel / passes) * unit_rows + wm * WROWS;
-  };
-  // The first segment by halving: later ones follow one by one.
-  int first_seg = 0;
-  if (u0 < u1) {
-    int lo = 0, hi = n_act - 1;
+  // A CTA's share of the chunks, moved down to where tiles begin: positions
+  // are (segment, tile), a segment's tiles counted pass after pass.
+  auto seg_chunks = [&](int s) { return ceil_div(s >= p.n_routed ? p.K_s : p.K, W4_CHUNK); };
+  auto boundary = [&](int b, int& seg, int& tile) {
+    const int at = (int)((long long)total * b / gridDim.x);
+    int lo = 0, hi = n_act;                          // the first segment that ends past `at`
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (u0 < tab[mid].x) hi = mid; else lo = mid + 1;
+      if (at < tab[mid].x) hi = mid; else lo = mid + 1;
     }
-    first_seg = lo;
-  }
+    seg = lo;
+    tile = lo < n_act ? (at - (lo ? tab[lo - 1].x : 0)) / seg_chunks(tab[lo].y) : 0;
+  };
+  int seg0, tile0, seg1, tile1;
+  boundary(blockIdx.x, seg0, tile0);
+  boundary(blockIdx.x + 1, seg1, tile1);
+  // The piece that begins at (seg, tile), which move past it; false at the end.
+  auto next_piece = [&](int& seg, int& tile, W4Piece& w) -> bool {
+    if (seg > seg1 || (seg == seg1 && tile >= tile1)) return false;
+    const W4Entry e = tab[seg];
+    w.dense = e.y >= p.n_routed;
+    w.op = w.dense ? p.w_s : p.w;
+    w.M = w.dense ? p.M_s : p.M;
+    w.K = w.dense ? p.K_s : p.K;
+    w.nch = ceil_div(w.K, W4_CHUNK);
+    w.row0 = w.dense ? 0 : (size_t)e.y * p.M;
+    const int per = ceil_div(w.M, WROWS), pass = tile / per;
+    int end = per * ceil_div(e.w, plan.rows);        // of the segment
+    const int last = seg == seg1 ? tile1 : end;
+    w.t0 = e.z + pass * plan.rows;
+    w.rows = min(plan.rows, e.w - pass * plan.rows);
+    w.tile0 = tile - pass * per;
+    w.tiles = min(last, (pass + 1) * per) - tile;
+    tile += w.tiles;
+    if (tile >= end) {
+      ++seg;
+      tile = 0;
+    }
+    return true;
+  };
+  auto share = [&](const W4Piece& w, int k) { return (int)((long long)w.tiles * w.nch * k / W4_WARPS); };
 
   // ------------------------------------------------------- weight stream
-  constexpr int NG = W4_CHUNK / GROUP;               // groups of a chunk: 2, 4 or 8
-  constexpr int PER = GROUP / 32;                    // steps of 32 k in a group
-  constexpr int HELD = NG > 4 ? 2 : 1;               // scales of a row that a lane loads: 4 lanes share a row's
-  int pu = u0, phint = first_seg, pc = 0, pn = 0, pK = 0, pgroups = 0;   // the next chunk: unit, index, count
-  const uint8_t* pq[2] = {nullptr, nullptr};         // this lane's pieces of codes, per tile
+  // The next chunk of this warp: the piece it is in, its tile and number, and
+  // how many more the warp has there. All lanes keep count, the first one
+  // starts the copies; each loads the scales of its rows, into registers.
+  int pseg = seg0, ptile = tile0, pc = 0, pleft = 0, pm = 0;
+  W4Piece pw = {};
   const uint16_t* psc[2] = {nullptr, nullptr};       // row g's scales
   const uint8_t* pz[2] = {nullptr, nullptr};         // and zero points, or null
-  uint16_t sc_r[2][2][HELD];                         // scales of the chunk under way: rows g and g + 8
-  uint8_t z_r[2][2][HELD];
-
-  auto open_unit = [&]() {                           // pointers of unit pu
-    W4Seg sg;
-    int m0;
-    locate(pu, phint, sg, m0);
-    pK = sg.K;
-    pn = ceil_div(sg.K, W4_CHUNK);
-    pgroups = sg.K / GROUP;
-    pc = wk;
+  int pgroups = 0;
+  // Scales and zero points of the last chunk started and of the one before it,
+  // rows g and g + 8, as loaded.
+  uint16_t sc_r[2][2][2][HELD] = {};
+  uint8_t z_r[2][2][2][HELD] = {};
+  auto open_tile = [&]() {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      const W4Operand& op = sg.op[MATS == 2 ? a : 0];
-      // A tile past the matrix (M is a multiple of 32) reads the first one: its
-      // products are not stored.
-      int m = MATS == 2 ? m0 : m0 + 16 * a;
-      if (m >= sg.M) m = 0;
-      const size_t row = sg.row0 + m;
-      pq[a] = op.q + (row + (lane >> 3)) * (size_t)(sg.K / 2) + (lane & 7) * 16 + pc * (W4_CHUNK / 2);
-      psc[a] = static_cast<const uint16_t*>(op.scale) + (row + g) * pgroups;
-      pz[a] = op.zero ? op.zero + (row + g) * pgroups : nullptr;
+      const W4Operand& op = pw.op[MATS == 2 ? a : 0];
+      const size_t row = pw.row0 + pm + (MATS == 2 ? 0 : 16 * a) + g;   // M is a multiple of 32
+      psc[a] = static_cast<const uint16_t*>(op.scale) + row * pgroups;
+      if (ZERO) pz[a] = op.zero ? op.zero + row * pgroups : nullptr;
     }
   };
-  // A tile in a stage: 128 bytes a row, its 16-byte pieces swapped about so
-  // that these writes and the word reads below each take every bank once.
-  const uint32_t ring_s = w4_smem(ring);
-  uint32_t put[2];                                   // rows lane / 8 + 8 i, and + 4
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = (lane >> 3) + 4 * h;
-    put[h] = r * 128 + (((lane & 7) ^ r) * 16);
-  }
-  // Start the next chunk of this warp's stream into stage `slot`: codes into
-  // shared memory, scales into registers, both used one chunk later.
+  const uint32_t ring_s = smem_u32(ring);
   auto issue = [&](int slot) {
-    while (pu < u1 && pc >= pn) {
-      if (++pu < u1) open_unit();
-    }
-    if (pu < u1) {
-      const uint32_t dst = ring_s + slot * W4_STAGE_BYTES;
-      const size_t row4 = (size_t)pK * 2;            // four rows of codes
-      if ((pc + 1) * W4_CHUNK <= pK) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            cp_async16_all(dst + a * W4_TILE_BYTES + (i >> 1) * 1024 + put[i & 1], pq[a] + i * row4);
-      } else {                                       // K ends inside the chunk
-        const bool in_k = pc * W4_CHUNK + (lane & 7) * 32 < pK;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            cp_async16_zfill(dst + a * W4_TILE_BYTES + (i >> 1) * 1024 + put[i & 1], pq[a] + i * row4 - (in_k ? 0 : (lane & 7) * 16), in_k);
-      }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        pq[a] += WK * (W4_CHUNK / 2);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < HELD; ++e) {
-          const int gi = min(pc * NG + (q & (NG / HELD - 1)) * HELD + e, pgroups - 1);
-          sc_r[a][0][e] = __ldg(psc[a] + gi);
-          sc_r[a][1][e] = __ldg(psc[a] + gi + 8 * pgroups);
-          z_r[a][0][e] = z_r[a][1][e] = 8;
-          if (pz[a]) {
-            z_r[a][0][e] = __ldg(pz[a] + gi);
-            z_r[a][1][e] = __ldg(pz[a] + gi + 8 * pgroups);
-          }
+          sc_r[0][a][h][e] = sc_r[1][a][h][e];
+          if (ZERO) z_r[0][a][h][e] = z_r[1][a][h][e];
+        }
+    while (pleft == 0) {                             // the next piece in which the warp has a share
+      if (!next_piece(pseg, ptile, pw)) return;
+      const int from = share(pw, warp);
+      pleft = share(pw, warp + 1) - from;
+      pgroups = pw.K / GROUP;
+      pm = (pw.tile0 + from / pw.nch) * WROWS;
+      pc = from % pw.nch;
+      if (pleft) open_tile();
+    }
+    if (lane == 0) {
+      const uint32_t fb = smem_u32(&full_bar[warp][slot]), dst = ring_s + slot * W4_STAGE_BYTES;
+      const int y = (int)pw.row0 + pm;
+      mbar_expect_tx(fb, W4_STAGE_BYTES);            // k past the matrix's end: zero fill
+      tma_load_2d(dst, pw.dense ? &tm0s : &tm0, pc * (W4_CHUNK / 2), y, fb);
+      if (MATS == 2) tma_load_2d(dst + W4_TILE_BYTES, pw.dense ? &tm1s : &tm1, pc * (W4_CHUNK / 2), y, fb);
+      else tma_load_2d(dst + W4_TILE_BYTES, pw.dense ? &tm0s : &tm0, pc * (W4_CHUNK / 2), y + 16, fb);
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int e = 0; e < HELD; ++e) {
+        const int gi = min(pc * NG + (q & (NG / HELD - 1)) * HELD + e, pgroups - 1);
+        sc_r[1][a][0][e] = __ldg(psc[a] + gi);
+        sc_r[1][a][1][e] = __ldg(psc[a] + gi + 8 * pgroups);
+        if (ZERO) {
+          z_r[1][a][0][e] = pz[a] ? __ldg(pz[a] + gi) : (uint8_t)8;
+          z_r[1][a][1][e] = pz[a] ? __ldg(pz[a] + gi + 8 * pgroups) : (uint8_t)8;
         }
       }
-      pc += WK;
+    --pleft;
+    if (++pc == pw.nch) {
+      pc = 0;
+      pm += WROWS;
+      if (pleft) open_tile();
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (pu < u1) open_unit();
-  issue(0);
-  if (p.wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i = 0; i < stages - 1; ++i) issue(i);
 
-  // ------------------------------------------------------------- products
-  const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-  const uint32_t get = g * 128 + q * 4;              // word q of row g's piece s: ^ (s ^ g) * 16
-  int slot = 0, hint = first_seg;
-  for (int u = u0; u < u1; ++u) {
-    W4Seg sg;
-    int m0;
-    locate(u, hint, sg, m0);
-    const uint4* xrow[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      // Token columns past the segment's rows read its first row: a column of
-      // the product takes nothing from its neighbours, and these are not stored.
-      const int r = t * 8 + g < sg.rows ? t * 8 + g : 0;
-      size_t src = sg.t0 + r;
-      if (!sg.dense && p.gather) {
-        const int v = p.gather[sg.t0 + r];
-        src = v >= 0 && v < p.gather_rows ? v : 0;
-      }
-      xrow[t] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s : p.x) +
-                                               src * (size_t)sg.K) + q;
-    }
-    float acc[2][NT][4];
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[a][t][i] = 0.0f;
-    const int nch = ceil_div(sg.K, W4_CHUNK);
-    for (int c = wk; c < nch; c += WK) {
-      uint32_t sc[2][HELD];                          // rows g and g + 8
-      float off[2][HELD][2];                         // with zero points: -scale (128 + zero), exact
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int e = 0; e < HELD; ++e) {
-          sc[a][e] = (uint32_t)sc_r[a][0][e] | ((uint32_t)sc_r[a][1][e] << 16);
-          if (p.has_zero)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              off[a][e][h] = __uint_as_float((uint32_t)sc_r[a][h][e] << 16) * (-128.0f - (float)(z_r[a][h][e] & 15));
-        }
-      issue(slot ^ 1);
-      const bool whole = (c + 1) * W4_CHUNK <= sg.K;
-      auto load_x = [&](int t, int s) -> uint4 {     // eight k of a token row
-        if (whole) return xrow[t][c * (W4_CHUNK / 8) + s * 4];
-        return c * W4_CHUNK + s * 32 < sg.K ? xrow[t][c * (W4_CHUNK / 8) + s * 4] : make_uint4(0, 0, 0, 0);
-      };
-      constexpr int AHEAD = NT == 1 ? 4 : 1;         // steps whose token rows are fetched ahead
-      uint4 xv[AHEAD];
-      if (NT == 1)
-#pragma unroll
-        for (int s = 0; s < AHEAD; ++s) xv[s] = load_x(0, s);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      __syncwarp();
-      const uint8_t* st = ring + slot * W4_STAGE_BYTES;
-      float grp[2][NT][4], xs[NT][4];
-#pragma unroll
-      for (int s = 0; s < W4_CHUNK / 32; ++s) {      // 32 codes of each row
-        uint32_t xb[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t > 0 && t * 8 >= sg.rows) break;
-          const uint4 v = NT == 1 ? xv[s % AHEAD] : load_x(t, s);
-          if (NT == 1 && s + AHEAD < W4_CHUNK / 32) xv[s % AHEAD] = load_x(0, s + AHEAD);
-          if (MATS == 2) {
-            xb[t][0] = __byte_perm(v.x, v.z, 0x5410);
-            xb[t][1] = __byte_perm(v.x, v.z, 0x7632);
-            xb[t][2] = __byte_perm(v.y, v.w, 0x5410);
-            xb[t][3] = __byte_perm(v.y, v.w, 0x7632);
-          } else {
-            xb[t][0] = v.x; xb[t][1] = v.y; xb[t][2] = v.z; xb[t][3] = v.w;
-          }
-          if (s % PER == 0) mma_16816_first(xs[t], ones, xb[t][0], xb[t][1]);
-          else mma_16816(xs[t], ones, xb[t][0], xb[t][1]);
-          mma_16816(xs[t], ones, xb[t][2], xb[t][3]);
-        }
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const uint8_t* w = st + a * W4_TILE_BYTES + (get ^ ((s ^ g) * 16));
-          uint32_t lo[4], hi[4];
-          unpack_w4(*reinterpret_cast<const uint32_t*>(w), lo);
-          unpack_w4(*reinterpret_cast<const uint32_t*>(w + 1024), hi);
-          const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (t > 0 && t * 8 >= sg.rows) break;
-            if (s % PER == 0) mma_16816_first(grp[a][t], a0, xb[t][0], xb[t][1]);
-            else mma_16816(grp[a][t], a0, xb[t][0], xb[t][1]);
-            mma_16816(grp[a][t], a1, xb[t][2], xb[t][3]);
-          }
-          if ((s + 1) % PER == 0) {                  // the group's sum is whole: its scale, from the lane that has it
-            const int sub = s / PER;
-            const uint32_t ss = __shfl_sync(0xffffffffu, sc[a][sub % HELD], (lane & 28) | (sub / HELD));
-            const float s0 = __uint_as_float(ss << 16), s1 = __uint_as_float(ss & 0xffff0000u);
-            float o0 = -136.0f * s0, o1 = -136.0f * s1;
-            if (p.has_zero) {
-              o0 = __shfl_sync(0xffffffffu, off[a][sub % HELD][0], (lane & 28) | (sub / HELD));
-              o1 = __shfl_sync(0xffffffffu, off[a][sub % HELD][1], (lane & 28) | (sub / HELD));
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              if (t > 0 && t * 8 >= sg.rows) break;
-              acc[a][t][0] = fmaf(s0, grp[a][t][0], fmaf(o0, xs[t][0], acc[a][t][0]));
-              acc[a][t][1] = fmaf(s0, grp[a][t][1], fmaf(o0, xs[t][1], acc[a][t][1]));
-              acc[a][t][2] = fmaf(s1, grp[a][t][2], fmaf(o1, xs[t][0], acc[a][t][2]));
-              acc[a][t][3] = fmaf(s1, grp[a][t][3], fmaf(o1, xs[t][1], acc[a][t][3]));
-            }
-          }
-        }
-      }
-      __syncwarp();                                  // every lane has read the stage
-      slot ^= 1;
-    }
-    // ------------------------------------------- the K shares meet, epilogue
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        red[warp * RED + (a * NT + t) * 32 + lane] =
-            make_float4(acc[a][t][0], acc[a][t][1], acc[a][t][2], acc[a][t][3]);
-    __syncthreads();
-    const int mu = m0 - wm * WROWS;                  // the unit's first weight row
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sg.dense ? p.out_s : p.out);
-    const float* redf = reinterpret_cast<const float*>(red);
-    for (int i = tid; i < sg.rows * unit_rows; i += W4_THREADS) {
-      const int n = i / unit_rows, m = i - n * unit_rows;
-      if (mu + m >= sg.M) continue;
-      const int r = m & 15, a = MATS == 1 ? (m >> 4) & 1 : 0, w0 = m / WROWS * WK;
-      const int at = ((n >> 3) * 32 + (r & 7) * 4 + ((n & 7) >> 1)) * 4 + (r >> 3) * 2 + (n & 1);
-      float v[2] = {0.0f, 0.0f};
-      for (int w = 0; w < WK; ++w) {
-        v[0] += redf[((w0 + w) * RED + a * NT * 32) * 4 + at];
-        if (MATS == 2) v[1] += redf[((w0 + w) * RED + NT * 32) * 4 + at];
-      }
-      // One rounding, of the activation (gate/up) or of the result (down).
-      const float o = MATS == 2 ? v[0] / (1.0f + __expf(-v[0])) * v[1] : v[0];
-      int col = mu + m;
-      if (MATS == 2) col = (col & ~7) | ((col & 3) * 2 + ((col >> 2) & 1));   // h in the down product's order of k
-      out[(size_t)(sg.t0 + n) * sg.M + col] = __float2bfloat16_rn(o);
-    }
-    __syncthreads();
-  }
-  // CTA 0 checks the caller's indices for all. Where no earlier kernel of the
-  // call could have left a code it writes the error word outright, which saves
-  // a launch that clears it.
-  if (p.err && blockIdx.x == 0) {
-    int bad = 0;
+  if (p.check && blockIdx.x == gridDim.x - 1) {
+    // The last CTA checks the caller's indices for all, before anything could
+    // time out. Where no earlier kernel of the call could have left a code it
+    // writes the error word outright, which saves a launch that clears it.
+    bool bad = false;
     for (int s = tid; s < p.n_routed; s += W4_THREADS) {
       const int a = p.offsets[s], b = p.offsets[s + 1];
       bad |= a < 0 || b < a || b > p.max_rows;
     }
     if (p.gather)
       for (int r = tid; r < p.max_rows; r += W4_THREADS) bad |= p.gather[r] < 0 || p.gather[r] >= p.gather_rows;
-    bad = __syncthreads_or(bad);
-    if (tid == 0) *p.err = (p.err_keep ? *p.err : 0u) | (bad ? kErrBadIndex : 0u);
+    if (bad) bad_word = 1;
+    __syncthreads();
+    if (tid == 0) *p.err = (p.err_keep ? *p.err : 0u) | (bad_word ? kErrBadIndex : 0u);
   }
+  if (p.wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ------------------------------------------------------------- token rows
+  // Row r of a piece by warp r % 8: its largest magnitude, then its values,
+  // eight k a lane paired as the codes are, and its groups' sums.
+  auto stage_rows = [&](const W4Piece& sg) {
+    for (int r = warp; r < sg.rows; r += W4_WARPS) {
+      size_t src = sg.t0 + r;
+      if (!sg.dense && p.gather) {
+        const int v = p.gather[sg.t0 + r];
+        src = v >= 0 && v < p.gather_rows ? v : 0;
+      }
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s : p.x) +
+                                                        src * (size_t)sg.K);
+      const int n8 = sg.K / 8;
+      uint32_t big = 0;                                  // bf16 magnitudes order like their bits, NaN above infinity
+#pragma unroll 4
+      for (int i = lane; i < n8; i += 32) {
+        const uint4 v = row[i];
+        big = __vmaxu2(__vmaxu2(big, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const uint32_t top = max(big & 0xffffu, big >> 16);
+      // 2^e top in [2^14, 2^15); e splits in two so that both factors are
+      // normal numbers, as does the power that the sums are multiplied by.
+      int e = top >= 0x0080u ? 14 - ((int)(top >> 7) - 127) : 140;
+      if (top >= 0x7f80u) e = 0;
+      const float f1 = __int_as_float((127 + e / 2) << 23), f2 = __int_as_float((127 + e - e / 2) << 23);
+      const int b = 24 - e;
+      if (lane == 0)
+        xfac[r] = make_float2(top >= 0x7f80u ? __int_as_float(0x7fc00000) : __int_as_float((127 + b / 2) << 23),
+                              __int_as_float((127 + b - b / 2) << 23));
+      uint8_t* to = xp + (size_t)r * plan.x_stride;
+      const int n8_pad = sg.nch * (W4_CHUNK / 8);
+#pragma unroll 2
+      for (int i = lane; i < n8_pad; i += 32) {          // whole warps: n8_pad is a multiple of 32
+        const uint4 v = i < n8 ? row[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float x[8], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[2 * j] = __uint_as_float(w[j] << 16) * f1 * f2;
+          x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * f1 * f2;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += x[j];
+        *reinterpret_cast<uint4*>(to + i * 16) =
+            make_uint4(half_pair(x[0], x[4]), half_pair(x[1] * 0.0625f, x[5] * 0.0625f), half_pair(x[2], x[6]),
+                       half_pair(x[3] * 0.0625f, x[7] * 0.0625f));
+#pragma unroll
+        for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (i % (GROUP / 8) == 0)
+          xsum[(i / (GROUP / 8)) * (8 * NT) + r] = sum * (ZERO ? -1.0f / 16777216.0f : -8.0f / 16777216.0f);
+      }
+    }
+  };
+
+  // ------------------------------------------------------------- products
+  uint32_t get[W4_CHUNK / 32];                       // word q of row g's piece s, pieces swapped by the swizzle
+#pragma unroll
+  for (int s = 0; s < W4_CHUNK / 32; ++s) get[s] = g * 128 + ((s ^ g) * 16) + q * 4;
+  const uint8_t* xlane = xp + (size_t)(g & (min(plan.rows, 8) - 1)) * plan.x_stride + q * 16;
+  int slot = 0, seg = seg0, tile = tile0;
+  uint32_t phase = 0;
+  bool ok = true;
+  W4Piece sg;
+  while (next_piece(seg, tile, sg)) {
+    stage_rows(sg);                                  // the last piece's barrier has freed the old rows
+    __syncthreads();
+    const int from = share(sg, warp), to = share(sg, warp + 1);
+    float acc[2][NT][4];
+    // A finished tile: lane's rows g and g + 8, token columns 2 q and 2 q + 1.
+    auto finish = [&](int m) {
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sg.dense ? p.out_s : p.out) + (size_t)sg.t0 * sg.M + m + g;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = t * 8 + q * 2 + (i & 1);
+          if (n >= sg.rows) continue;
+          const float2 fac = xfac[n];
+          const float v0 = acc[0][t][i] * fac.x * fac.y, v1 = acc[1][t][i] * fac.x * fac.y;
+          __nv_bfloat16* at = out + (size_t)n * sg.M + (i >> 1) * 8;
+          // One rounding, of the activation (gate/up) or of the result (down).
+          if (MATS == 2) {
+            at[0] = __float2bfloat16_rn(v0 / (1.0f + __expf(-v0)) * v1);
+          } else {
+            at[0] = __float2bfloat16_rn(v0);
+            at[16] = __float2bfloat16_rn(v1);
+          }
+        }
+    };
+    int c = from % sg.nch, m = (sg.tile0 + from / sg.nch) * WROWS;
+    bool began = c == 0;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[a][t][i] = 0.0f;
+    for (int k = from; k < to; ++k) {
+      uint32_t sc[2][HELD];                          // rows g and g + 8
+      float zp[2][HELD][2];
+      const int newest = 3 - stages;                 // 1: two stages, this chunk is the last one started
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < HELD; ++e) {
+          const uint32_t s0 = newest ? sc_r[1][a][0][e] : sc_r[0][a][0][e];
+          const uint32_t s1 = newest ? sc_r[1][a][1][e] : sc_r[0][a][1][e];
+          sc[a][e] = s0 | (s1 << 16);
+          if (ZERO) {
+            zp[a][e][0] = (float)((newest ? z_r[1][a][0][e] : z_r[0][a][0][e]) & 15);
+            zp[a][e][1] = (float)((newest ? z_r[1][a][1][e] : z_r[0][a][1][e]) & 15);
+          }
+        }
+      if (ok) issue(slot == 0 ? stages - 1 : slot - 1);
+      ok = ok && warp_wait(smem_u32(&full_bar[warp][slot]), phase, abort_flag, p.err, p.timeout_ns);
+      const uint8_t* st = ring + slot * W4_STAGE_BYTES;
+      const uint8_t* xc = xlane + c * (2 * W4_CHUNK);
+      const float* xsc = xsum + c * NG * (8 * NT) + q * 2;
+      float grp[2][NT][4];
+#pragma unroll
+      for (int s = 0; s < W4_CHUNK / 32; ++s) {      // 32 codes of each row
+        uint4 xb[NT];
+        // Minus eight times a group's sum of activations (or minus once, where
+        // there are zero points to multiply it): where its products start from.
+        float2 xs[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (t > 0 && t * 8 >= sg.rows) break;
+          xb[t] = *reinterpret_cast<const uint4*>(xc + (size_t)t * 8 * plan.x_stride + s * 64);
+          if (s % PER == 0) xs[t] = *reinterpret_cast<const float2*>(xsc + (s / PER) * (8 * NT) + t * 8);
+        }
+        const int sub = s / PER, from_lane = (lane & 28) | (sub / HELD);   // the lane that has the group's scales
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const uint8_t* w = st + a * W4_TILE_BYTES + get[s];
+          uint32_t lo[4], hi[4];
+          unpack_w4(*reinterpret_cast<const uint32_t*>(w), lo);
+          unpack_w4(*reinterpret_cast<const uint32_t*>(w + 1024), hi);
+          const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+          float z0 = 1.0f, z1 = 1.0f;
+          if (ZERO && s % PER == 0) {
+            z0 = __shfl_sync(0xffffffffu, zp[a][sub % HELD][0], from_lane);
+            z1 = __shfl_sync(0xffffffffu, zp[a][sub % HELD][1], from_lane);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (t > 0 && t * 8 >= sg.rows) break;
+            if (s % PER == 0) {
+              if (ZERO) mma_f16_from(grp[a][t], a0, xb[t].x, xb[t].y, z0 * xs[t].x, z0 * xs[t].y, z1 * xs[t].x, z1 * xs[t].y);
+              else mma_f16_from(grp[a][t], a0, xb[t].x, xb[t].y, xs[t].x, xs[t].y, xs[t].x, xs[t].y);
+            } else {
+              mma_f16(grp[a][t], a0, xb[t].x, xb[t].y);
+            }
+            mma_f16(grp[a][t], a1, xb[t].z, xb[t].w);
+          }
+          if ((s + 1) % PER == 0) {                  // the group's sum is whole
+            const uint32_t ss = __shfl_sync(0xffffffffu, sc[a][sub % HELD], from_lane);
+            const float s0 = __uint_as_float(ss << 16), s1 = __uint_as_float(ss & 0xffff0000u);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if (t > 0 && t * 8 >= sg.rows) break;
+              acc[a][t][0] = fmaf(s0, grp[a][t][0], acc[a][t][0]);
+              acc[a][t][1] = fmaf(s0, grp[a][t][1], acc[a][t][1]);
+              acc[a][t][2] = fmaf(s1, grp[a][t][2], acc[a][t][2]);
+              acc[a][t][3] = fmaf(s1, grp[a][t][3], acc[a][t][3]);
+            }
+          }
+        }
+      }
+      __syncwarp();                                  // every lane has read the stage
+      if (++slot == stages) { slot = 0; phase ^= 1u; }
+      if (++c == sg.nch) {                           // the tile ends
+        if (began) {
+          finish(m);
+        } else {
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              red[warp * RED + (a * NT + t) * 32 + lane] =
+                  make_float4(acc[a][t][0], acc[a][t][1], acc[a][t][2], acc[a][t][3]);
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[a][t][i] = 0.0f;
+        c = 0;
+        m += WROWS;
+        began = true;
+      }
+    }
+    const bool open = c > 0 && from < to;            // the share ends inside a tile
+    if (open && !began) {                            // and began inside the same one
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          red[warp * RED + (a * NT + t) * 32 + lane] =
+              make_float4(acc[a][t][0], acc[a][t][1], acc[a][t][2], acc[a][t][3]);
+    }
+    __syncthreads();                                 // left sums visible, token rows free
+    if (open && began) {
+      // The tile's other shares, in order: the warps whose shares begin before
+      // its end.
+      const int end = (to / sg.nch + 1) * sg.nch;
+      for (int w = warp + 1; w < W4_WARPS && share(sg, w) < end; ++w) {
+        if (share(sg, w) == share(sg, w + 1)) continue;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float4 v = red[w * RED + (a * NT + t) * 32 + lane];
+            acc[a][t][0] += v.x;
+            acc[a][t][1] += v.y;
+            acc[a][t][2] += v.z;
+            acc[a][t][3] += v.w;
+          }
+      }
+      finish(m);
+    }
+    __syncthreads();                                 // left sums and factors free
+  }
+  // After a wait that ran out: the copies under way land (or have had two more
+  // seconds) before shared memory is freed.
+  if (!ok && lane == 0)
+    for (int i = 0; i < stages; ++i)
+      wait_bounded(smem_u32(&full_bar[warp][(slot + i) % stages]), phase ^ (slot + i >= stages ? 1u : 0u), abort_flag,
+                   p.err, p.timeout_ns, false);
 }
 
-template <int NT> int w4_smem_bytes(int n_seg) {
-  return W4_WARPS * (W4_STAGES * W4_STAGE_BYTES + 2 * NT * 512) + n_seg * (int)sizeof(W4Entry);
+// Codes [rows][K/2] as bytes, 128-byte swizzle, box 128 bytes x 16 rows.
+bool make_w4_tmap(CUtensorMap* tm, const void* q, long long rows, int K) {
+  auto fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+  cuuint32_t box[2] = {W4_CHUNK / 2, 16};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Experts that a batch is expected to touch under even routing.
@@ -445,48 +585,69 @@ double w4_touched(const W4GemmParams& p) {
   return p.n_routed * (1.0 - pow(1.0 - 1.0 / p.n_routed, (double)p.max_rows));
 }
 
-// Token tiles of eight per unit. A segment with more rows takes its weights
-// again for every 8 NT of them, a unit with more tiles does more products per
-// weight: 1, 1.3 and 2.1 times the time of one tile, measured at d = 7168 with
-// 8, 16 and 32 rows an expert. Routed segments vary about their mean.
-int w4_token_tiles(const W4GemmParams& p) {
-  const double act = w4_touched(p), cost[3] = {1.0, 1.3, 2.1};
-  int best = 1;
-  double least = 1e300;
-  for (int i = 0; i < 3; ++i) {
-    const int nt = 1 << i;
-    double t = (double)p.M_s * p.K_s * ceil_div(p.dense_rows, 8 * nt);
-    if (act > 0.0) {
-      const double mean = p.max_rows / act, passes = (mean + sqrt(mean)) / (8.0 * nt);
-      t += act * p.M * p.K * (passes > 1.0 ? passes : 1.0);
-    }
-    t *= cost[i];
-    if (t < least) {
-      least = t;
-      best = nt;
-    }
-  }
-  return best;
+constexpr int W4_SMEM = 224 * 1024, W4_SMEM_HALF = 115000;   // of one CTA an SM, of two
+
+int w4_layout(const W4GemmParams& p, int nt, int rows, int stages, W4Plan& l) {
+  const int K = p.n_routed > 0 && p.K > p.K_s ? p.K : (p.dense_rows > 0 && p.K_s > p.K ? p.K_s : p.K);
+  const int pad = ceil_div(K, W4_CHUNK) * W4_CHUNK;
+  int off = 0;
+  auto take = [&](int bytes) {
+    const int o = off;
+    off += ceil_div(bytes, 128) * 128;
+    return o;
+  };
+  l.stages = stages;
+  l.rows = rows;
+  l.x_stride = 2 * pad + 64;                // 64 past a multiple of 128: a pair of rows takes every bank once
+  take(W4_WARPS * stages * W4_STAGE_BYTES);
+  l.red = take(W4_WARPS * 2 * nt * 512);
+  l.x = take(rows * l.x_stride);
+  l.xs = take(pad / p.group * 8 * nt * 4);
+  l.f = take(8 * nt * 8);
+  l.tab = take((p.n_routed + (p.dense_rows > 0 ? 1 : 0)) * (int)sizeof(W4Entry));
+  return off + 1024;                        // the rings start on a multiple of 1024
 }
 
-// Warps along K. A CTA's time is its units times a warp's chunks in each (and
-// about half a chunk of joining the shares); the split that makes this
-// smallest for the experts that the batch is expected to touch wins.
-int w4_split(const W4GemmParams& p, int slots) {
-  const double act = w4_touched(p);
-  int best = 1;
+struct W4Shape {
+  W4Plan plan;
+  int nt, ctas, smem;
+};
+
+// Token tiles of eight per pass, and CTAs an SM. More token tiles do more
+// products a weight (1, 1.3 and 2 times the time of one), fewer passes over a
+// segment's weights; token rows that do not fit twice in an SM's shared memory
+// leave one CTA there (1.4 times the time), those that do not fit at all take
+// fewer rows a pass. Routed segments vary about their mean.
+bool w4_shape(const W4GemmParams& p, W4Shape& best) {
+  const double act = w4_touched(p), cost[3] = {1.0, 1.3, 2.0};
   double least = 1e300;
-  for (int wk = 1; wk <= W4_WARPS; wk *= 2) {
-    const int rows = (p.mats == 2 ? 16 : 32) * (W4_WARPS / wk);
-    const double units = act * ceil_div(p.M, rows) + (p.dense_rows > 0 ? ceil_div(p.M_s, rows) : 0);
-    const int K = p.n_routed > 0 ? p.K : p.K_s;
-    const double t = ceil(units / slots) * (ceil_div(ceil_div(K, W4_CHUNK), wk) + 0.5);
+  for (int i = 0; i < 3; ++i) {
+    W4Shape s;
+    s.nt = 1 << i;
+    int rows = 8 * s.nt;
+    while (rows > 1 && w4_layout(p, s.nt, rows, 2, s.plan) > W4_SMEM) rows /= 2;
+    if (s.nt > 1 && rows < 8 * s.nt) break;
+    s.smem = w4_layout(p, s.nt, rows, 2, s.plan);
+    if (s.smem > W4_SMEM) break;
+    s.ctas = s.smem <= W4_SMEM_HALF ? 2 : 1;
+    W4Plan deep;                            // a third stage where there is room
+    const int n = w4_layout(p, s.nt, rows, W4_MAX_STAGES, deep);
+    if (n <= (s.ctas == 2 ? W4_SMEM_HALF : W4_SMEM)) {
+      s.plan = deep;
+      s.smem = n;
+    }
+    double t = (double)p.M_s * p.K_s * ceil_div(p.dense_rows, rows);
+    if (act > 0.0) {
+      const double mean = p.max_rows / act, passes = (mean + sqrt(mean)) / rows;
+      t += act * p.M * p.K * (passes > 1.0 ? passes : 1.0);
+    }
+    t *= cost[i] * (s.ctas == 1 ? 1.4 : 1.0);
     if (t < least) {
       least = t;
-      best = wk;
+      best = s;
     }
   }
-  return best;
+  return least < 1e300;
 }
 
 // ------------------------------------------------------ making the weights
@@ -628,39 +789,50 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(const uint32_t* __re
 }  // namespace
 
 cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
-  const int slots = 2 * num_sms;
-  const int nt = w4_token_tiles(p);
-  const int wk = w4_split(p, slots);
-  const int n_seg = p.n_routed + (p.dense_rows > 0 ? 1 : 0);
-  auto go = [&](auto tag, int smem) {
+  W4Shape shape;
+  if (!w4_shape(p, shape)) return cudaErrorInvalidValue;
+  const int slots = shape.ctas * num_sms;
+  CUtensorMap tm[4];
+  for (int a = 0; a < 2; ++a) {
+    if (a < p.mats) {
+      if (!make_w4_tmap(&tm[a], p.w[a].q, (long long)p.n_routed * p.M, p.K)) return cudaErrorInvalidValue;
+      if (p.dense_rows > 0 && !make_w4_tmap(&tm[2 + a], p.w_s[a].q, p.M_s, p.K_s)) return cudaErrorInvalidValue;
+    } else {
+      tm[a] = tm[0];
+    }
+    if (a >= p.mats || p.dense_rows == 0) tm[2 + a] = p.dense_rows > 0 ? tm[2] : tm[a];
+  }
+  auto go = [&](auto tag) {
     constexpr auto kernel = decltype(tag)::value;
     const cudaError_t e = allow_max_smem<kernel>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(slots);
     cfg.blockDim = dim3(W4_THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = shape.smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.wait_previous ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p, wk);
+    return cudaLaunchKernelEx(&cfg, kernel, tm[0], tm[1], tm[2], tm[3], p, shape.plan);
   };
-  auto with = [&](auto mats, auto n) {
+  auto with = [&](auto mats, auto n, auto zero) {
     constexpr int M = decltype(mats)::value, N = decltype(n)::value;
-    const int smem = w4_smem_bytes<N>(n_seg);
-    return p.group == 128  ? go(KernelTag<w4_gemm_kernel<M, N, 128>>{}, smem)
-           : p.group == 64 ? go(KernelTag<w4_gemm_kernel<M, N, 64>>{}, smem)
-                           : go(KernelTag<w4_gemm_kernel<M, N, 32>>{}, smem);
+    constexpr bool Z = decltype(zero)::value;
+    return p.group == 128  ? go(KernelTag<w4_gemm_kernel<M, N, 128, Z>>{})
+           : p.group == 64 ? go(KernelTag<w4_gemm_kernel<M, N, 64, Z>>{})
+                           : go(KernelTag<w4_gemm_kernel<M, N, 32, Z>>{});
   };
-  auto rows_of = [&](auto n) {
-    return p.mats == 2 ? with(std::integral_constant<int, 2>{}, n) : with(std::integral_constant<int, 1>{}, n);
+  auto mats = [&](auto n, auto zero) {
+    return p.mats == 2 ? with(std::integral_constant<int, 2>{}, n, zero)
+                       : with(std::integral_constant<int, 1>{}, n, zero);
   };
-  return nt == 1   ? rows_of(std::integral_constant<int, 1>{})
-         : nt == 2 ? rows_of(std::integral_constant<int, 2>{})
-                   : rows_of(std::integral_constant<int, 4>{});
+  auto rows_of = [&](auto n) { return p.has_zero ? mats(n, std::true_type{}) : mats(n, std::false_type{}); };
+  return shape.nt == 1   ? rows_of(std::integral_constant<int, 1>{})
+         : shape.nt == 2 ? rows_of(std::integral_constant<int, 2>{})
+                         : rows_of(std::integral_constant<int, 4>{});
 }
 
 cudaError_t launch_w4_quantize(int dtype, const void* w, long long n, int group, void* q, void* scale, void* zero,

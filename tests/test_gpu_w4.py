@@ -1,10 +1,13 @@
 """4-bit expert weights on the GPU against the fp64 oracle.
 
-Bounds of the expert FFN. The products run over 128 + code, exact in bf16, and
-128 + zero times the group's sum of activations comes off in fp32: every
-product is exact, and each addition is off by at most one unit of 2^-23 (the
-tensor cores' adder may truncate) of the absolute terms. A group's two sums
-have terms of at most 143 |x| and G / 16 + 4 additions in a row; their
+Bounds of the expert FFN. A token row runs in fp16 under a
+power of two for the row, a part of it under 1/16 besides: exact, but for values
+below 2^-17 16 / 2^14 = 2^-27 of the row's largest magnitude, which are off by at
+most 2^-25 16 / 2^14 = 2^-35 of that. The codes are
+exact, so every product of a group is exact, and each addition is off by at
+most one unit of 2^-23 (the tensor cores' adder may truncate) of the absolute
+terms. A group's sum, and the zero point times its activations' sum that comes
+off it, have terms of at most 15 |x| and G / 8 + 8 additions in a row; their
 difference, scaled, takes at most K / 16 + 16 more over |W| |x|. SiLU's slope is below 1.1, its fp32 evaluation
 good to 2^-20. The intermediate is rounded to bf16 (2^-8 of its size at most),
 passes through |W2|, and the result is rounded once more.
@@ -130,10 +133,12 @@ def check_rows(got, x, w1, w3, w2, what, s1, s3, s2, group):
     y, a, b, h = lo.swiglu_rows(x, w1, w3, w2)
     units = lambda K: (K / 16 + 16) * 2.0 ** -23
     K, f = x.shape[1], h.shape[1]
-    in_group = (group / 16 + 4) * 2.0 ** -23 * 2 * 143
-    ea, eb = (units(K) * (np.abs(x) @ np.abs(w).T) + in_group * (np.abs(x) @ s.T) for w, s in ((w1, s1), (w3, s3)))
+    in_group = (group / 8 + 8) * 2.0 ** -23 * 2 * 15
+    split = lambda v, w: 2.0 ** -35 * np.abs(v).max(-1, keepdims=True) * np.abs(w).sum(-1)
+    ea, eb = (units(K) * (np.abs(x) @ np.abs(w).T) + in_group * (np.abs(x) @ s.T) + split(x, w)
+              for w, s in ((w1, s1), (w3, s3)))
     eh = 1.1 * ea * (np.abs(b) + eb) + np.abs(h) / np.maximum(np.abs(b), 1e-300) * eb + (2.0 ** -8 + 2.0 ** -20) * np.abs(h)
-    ey = eh @ np.abs(w2).T + units(f) * (np.abs(h) @ np.abs(w2).T) + in_group * (np.abs(h) @ s2.T) + 2.0 ** -8 * np.abs(y) + 1e-38
+    ey = eh @ np.abs(w2).T + units(f) * (np.abs(h) @ np.abs(w2).T) + in_group * (np.abs(h) @ s2.T) + split(h, w2) + 2.0 ** -8 * np.abs(y) + 1e-38
     got = f64(got)
     assert np.isfinite(got).all(), what
     assert (np.abs(got - y) <= ey).all(), (what, (np.abs(got - y) - ey).max())
@@ -169,6 +174,7 @@ CASES = [  # T, d, E, k, f, f_shared, group, zeros
     (17, 640, 2, 2, 256, 128, 128, False), (31, 2048, 16, 4, 768, 0, 128, False), (40, 512, 300, 8, 64, 64, 64, True),
     (33, 1152, 4, 3, 640, 384, 128, True), (100, 320, 6, 2, 96, 96, 32, False), (300, 256, 4, 2, 256, 128, 64, False),
     (5, 7168, 4, 2, 2048, 256, 128, False), (24, 4096, 3, 1, 1536, 0, 32, True),
+    (11, 14336, 2, 1, 96, 0, 32, False), (3, 16384, 2, 2, 64, 64, 32, True), (64, 2048, 4, 2, 512, 0, 128, False),
 ]
 
 
@@ -203,6 +209,37 @@ def test_rows_behind_the_last_segment_stay_and_infinities_stay_in_their_row():
     clean = (perm_src[:n] != 3) & (perm_src[:n] != 4)
     assert torch.equal(out[:n][clean], y[:n][clean])
     assert not torch.isfinite(out[:n][~clean].float()).all(dim=1).any()
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 3e-3, 1.0, 1e3, 1e28])
+def test_rows_of_any_magnitude(scale):
+    # Row by row another size, one row of zeros, one of a single large value;
+    # the largest stay where the products themselves are finite.
+    cfg, x, w, ws, perm_src, offsets = make(10, 512, 4, 2, 128, 0, 64, True, seed=7)
+    rows = torch.tensor([1, 2, 4, 0.5, 1e-2, 0, 1, 1, 30, 1e-4], device="cuda")[:, None]
+    xs = (x.float() * rows * scale)
+    xs[6] = 0
+    xs[6, 100] = scale
+    xs = xs.to(BF)
+    xp, off = xs[perm_src.long()], offsets.tolist()
+    wk = B.alloc_workspace(cfg)
+    # h grows with the square of x: only the pre-activations' scale is kept
+    # apart here, by weights w3 whose scale undoes it.
+    w3 = B.W4Matrix(w[1].q, (w[1].scale.float() / scale).to(BF) if scale in (1e3, 1e28) else w[1].scale, w[1].zero, 64)
+    ww = [w[0], w3, w[2]]
+    y = torch.full((20, 512), float("nan"), device="cuda", dtype=BF)
+    B.moe_expert_swiglu_w4(cfg, xs, perm_src, offsets, *ww, None, *ws, y, None, wk)
+    for e in range(4):
+        if off[e] < off[e + 1]:
+            with np.errstate(over="ignore"):
+                want, a, b, h = lo.swiglu_rows(f64(xp[off[e]:off[e + 1]]), *[dense(m, e) for m in ww])
+            got = f64(y[off[e]:off[e + 1]])
+            assert np.isfinite(got).all()
+            # Relative to each row's largest result: two roundings to bf16 (as
+            # above), the split and SiLU's fp32 evaluation stay below 2^-6 of
+            # it; below 1e-37 bf16 and fp32 have subnormal numbers only.
+            room = 2.0 ** -6 * np.abs(want).max(-1, keepdims=True) + 1e-37
+            assert (np.abs(got - want) <= room).all(), e
 
 
 def test_bad_tables_are_reported():

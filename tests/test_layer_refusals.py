@@ -122,7 +122,7 @@ def test_w4_matrix_shapes(rows, K, dtype, group, status):
 @pytest.mark.parametrize("m,w,status", [
     (None, FAKE, B.MOE_ERR_INVALID_ARG), (w4(q=None), FAKE, B.MOE_ERR_INVALID_ARG),
     (w4(scale=None), FAKE, B.MOE_ERR_INVALID_ARG), (w4(q=ODD), FAKE, B.MOE_ERR_MISALIGNED),
-    (w4(scale=ODD), FAKE, B.MOE_ERR_MISALIGNED), (w4(), None, B.MOE_ERR_INVALID_ARG), (w4(), ODD, B.MOE_ERR_MISALIGNED)])
+    (w4(scale=ODD), FAKE, B.MOE_ERR_MISALIGNED), (w4(zero=ODD), FAKE, B.MOE_ERR_MISALIGNED), (w4(), None, B.MOE_ERR_INVALID_ARG), (w4(), ODD, B.MOE_ERR_MISALIGNED)])
 def test_w4_matrix_pointers(m, w, status):
     L = B.lib()
     assert L.moe_w4_quantize(4, 128, 0, 64, w, m, None) == status
@@ -152,7 +152,7 @@ def call_forward_w4(cfg, group=64, **kw):
 @pytest.mark.parametrize("kw,group,status", [
     (dict(k=5), 64, B.MOE_ERR_INVALID_ARG), ({}, 16, B.MOE_ERR_INVALID_ARG), ({}, 256, B.MOE_ERR_INVALID_ARG),
     (dict(dtype=B.MOE_DTYPE_F32), 64, B.MOE_ERR_UNSUPPORTED), (dict(d=96), 64, B.MOE_ERR_UNSUPPORTED),
-    (dict(f=288), 64, B.MOE_ERR_UNSUPPORTED), (dict(f_shared=96), 64, B.MOE_ERR_UNSUPPORTED)])
+    (dict(f=288), 64, B.MOE_ERR_UNSUPPORTED), (dict(f=16448), 64, B.MOE_ERR_UNSUPPORTED), (dict(f_shared=96), 64, B.MOE_ERR_UNSUPPORTED)])
 def test_w4_experts_settings(kw, group, status):
     assert call_experts_w4(moe_cfg(**kw), group) == status
     assert call_forward_w4(moe_cfg(**kw), group) == status
