@@ -597,6 +597,7 @@ class W4Matrix:
         self.q, self.scale, self.zero, self.group = q, scale, zero, group
         self.K = 2 * q.shape[-1]
         self.rows = q.numel() // q.shape[-1] if q.numel() else 0
+        self._key = None
         for t, name in ((scale, "scale"), (zero, "zero")):
             if t is not None and t.numel() != self.rows * (self.K // group):
                 raise ValueError(f"{name}: {t.numel()} elements, expected {self.rows * (self.K // group)}")
@@ -619,11 +620,18 @@ class W4Matrix:
         return m
 
     def _c(self):
-        """Reference to the C struct, with the tensors' addresses of now."""
-        q, scale, zero = _args((self.q, "q", self.rows * (self.K // 2), _U8, True),
-                               (self.scale, "scale", self.rows * (self.K // self.group), torch.bfloat16, True),
-                               (self.zero, "zero", self.rows * (self.K // self.group), _U8, False))
-        return ctypes.byref(CW4Matrix(q, scale, zero))
+        """Reference to the C struct, with the tensors' addresses of now: checked
+        anew when a tensor, its address or the current device is another one."""
+        q, scale, zero = self.q, self.scale, self.zero
+        key = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(), id(q), id(scale), id(zero),
+               torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2)
+        if key != self._key:
+            groups = self.rows * (self.K // self.group)
+            a = _args((q, "q", self.rows * (self.K // 2), _U8, True), (scale, "scale", groups, torch.bfloat16, True),
+                      (zero, "zero", groups, _U8, False))
+            self._struct = CW4Matrix(*a)
+            self._ref, self._key = ctypes.byref(self._struct), key
+        return self._ref
 
 
 def _dense_code(w, name: str) -> int:

@@ -332,10 +332,12 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
   if (p.wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ------------------------------------------------------------- token rows
-  // Row r of a piece by warp r % 8: its largest magnitude, then its values,
-  // eight k a lane paired as the codes are, and its groups' sums.
+  // A row of a piece by one warp, or by 2, 4 or 8 where there are as few rows:
+  // its largest magnitude (each of them), then its values, eight k a lane paired
+  // as the codes are, and its groups' sums (each a share).
   auto stage_rows = [&](const W4Piece& sg) {
-    for (int r = warp; r < sg.rows; r += W4_WARPS) {
+    const int team = sg.rows > 4 ? 1 : sg.rows > 2 ? 2 : sg.rows > 1 ? 4 : 8;
+    for (int r = warp / team; r < sg.rows; r += W4_WARPS / team) {
       size_t src = sg.t0 + r;
       if (!sg.dense && p.gather) {
         const int v = p.gather[sg.t0 + r];
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
                                                         src * (size_t)sg.K);
       const int n8 = sg.K / 8;
       uint32_t big = 0;                                  // bf16 magnitudes order like their bits, NaN above infinity
-#pragma unroll 4
+#pragma unroll 8
       for (int i = lane; i < n8; i += 32) {
         const uint4 v = row[i];
         big = __vmaxu2(__vmaxu2(big, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
@@ -360,13 +362,13 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
       if (top >= 0x7f80u) e = 0;
       const float f1 = __int_as_float((127 + e / 2) << 23), f2 = __int_as_float((127 + e - e / 2) << 23);
       const int b = 24 - e;
-      if (lane == 0)
+      if (lane == 0 && warp % team == 0)
         xfac[r] = make_float2(top >= 0x7f80u ? __int_as_float(0x7fc00000) : __int_as_float((127 + b / 2) << 23),
                               __int_as_float((127 + b - b / 2) << 23));
       uint8_t* to = xp + (size_t)r * plan.x_stride;
       const int n8_pad = sg.nch * (W4_CHUNK / 8);
 #pragma unroll 2
-      for (int i = lane; i < n8_pad; i += 32) {          // whole warps: n8_pad is a multiple of 32
+      for (int i = (warp % team) * 32 + lane; i < n8_pad; i += 32 * team) {   // whole warps: n8_pad is a multiple of 32
         const uint4 v = i < n8 ? row[i] : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         float x[8], sum = 0.0f;
