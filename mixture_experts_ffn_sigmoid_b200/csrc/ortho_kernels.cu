@@ -32,6 +32,11 @@
 // of K, six stages), two accumulators in TMEM so that the epilogue of a tile
 // runs under the next one's MMAs. X is the MN-major operand of B X, so it is
 // stored once. The last step's epilogue writes the result or the weights.
+//
+// Matrices of up to 128 x 512 (either way round) stay in shared memory from the
+// first read to the last write: one launch, one CTA a matrix (ns_chip_kernel).
+// Their products are too short for launches between them: 8 matrices of 256 x
+// 128 took 97 us in 17 launches.
 #include <cuda_fp16.h>
 
 #include "umma_common.cuh"
@@ -536,6 +541,242 @@ __global__ void __launch_bounds__(256) ns_init_kernel(const T* __restrict__ g, c
   }
 }
 
+// ------------------------------------------------- small matrices, on chip
+constexpr int NSC_THREADS = 512;
+constexpr int NSC_M = 128, NSC_N = 512;
+constexpr int NSC_BLOCK = NSC_M * 128;             // 64 columns of 128 rows
+constexpr int NSC_SMEM = 1024 + (NSC_N / 64 + 2 * (NSC_M / 64)) * NSC_BLOCK;
+
+// Element (r, c) of a matrix in blocks of 64 columns x 128 rows, 128-byte
+// swizzle: K-major as it stands, and MN-major with its columns as N.
+__device__ __forceinline__ uint32_t nsc_at(int r, int c) {
+  return (uint32_t)((c >> 6) * NSC_BLOCK + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) * 16) + (c & 7) * 2);
+}
+// MN-major operand whose 64-column groups are a block apart.
+__device__ __forceinline__ uint64_t nsc_mn_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(NSC_BLOCK >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+struct NsChipParams {
+  NsGemmParams g;
+  const void* grad;
+  float* mom;
+  float mu, eps;
+  int nesterov, steps, clear_err;
+  float coeffs[3 * 64];
+};
+
+// One matrix per CTA: X [128][64 k] stays in shared memory, A and B beside it;
+// each product's accumulator (128 rows, up to 512 columns of TMEM) goes through
+// registers back into the operand it becomes. Thread 0 issues the MMAs, all 16
+// warps move the results: lane quarter warp % 4, every fourth 32 columns.
+template <typename T, bool MOM>
+__global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_constant__ NsChipParams cp) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ float red[NSC_THREADS / 32];
+  __shared__ uint64_t done_bar;
+  __shared__ uint32_t tmem_slot, abort_word;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const NsGemmParams& p = cp.g;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, mat = blockIdx.x;
+  const int nb = ceil_div(p.n, 64);
+  uint8_t *xs = smem, *as = smem + (NSC_N / 64) * NSC_BLOCK, *bs = as + (NSC_M / 64) * NSC_BLOCK;
+  volatile uint32_t* abort_flag = &abort_word;
+  if (tid == 0) {
+    mbar_init(smem_u32(&done_bar), 1);
+    abort_word = 0u;
+    if (cp.clear_err && mat == 0) *p.err = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  for (int i = tid; i < (nb + 2 * (NSC_M / 64)) * (NSC_BLOCK / 16); i += NSC_THREADS)   // rows and columns past the matrix
+    reinterpret_cast<uint4*>(i < nb * (NSC_BLOCK / 16) ? xs : as - nb * NSC_BLOCK)[i] = make_uint4(0, 0, 0, 0);
+
+  // ------------------------------------------------------ norm, then X
+  const size_t size = (size_t)p.rows * p.cols, base = (size_t)mat * size;
+  const T* grad = static_cast<const T*>(cp.grad) + base;
+  float* mom = MOM ? cp.mom + base : nullptr;
+  const bool vec = p.cols % 8 == 0;
+  const int per_row = ceil_div(p.cols, 8), groups = p.rows * per_row;
+  // Eight columns of a row of U; `first`: the momentum moves on.
+  auto load_u = [&](int i, bool first, float (&f)[8], int& r, int& c) {
+    r = i / per_row;
+    c = (i - r * per_row) * 8;
+    const size_t at = (size_t)r * p.cols + c;
+    const int n = min(8, p.cols - c);
+    float m[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = m[e] = 0.0f;
+    if (vec) {
+      ns_load8(grad + at, f);
+      if (MOM) ns_load8(mom + at, m);
+    } else {
+      for (int e = 0; e < n; ++e) {
+        f[e] = to_f32(grad[at + e]);
+        if (MOM) m[e] = mom[at + e];
+      }
+    }
+    if (MOM) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (first) m[e] = fmaf(cp.mu, m[e], f[e]);
+        f[e] = cp.nesterov ? fmaf(cp.mu, m[e], f[e]) : m[e];
+      }
+      if (first) {
+        if (vec) {
+          reinterpret_cast<float4*>(mom + at)[0] = make_float4(m[0], m[1], m[2], m[3]);
+          reinterpret_cast<float4*>(mom + at)[1] = make_float4(m[4], m[5], m[6], m[7]);
+        } else {
+          for (int e = 0; e < n; ++e) mom[at + e] = m[e];
+        }
+      }
+    }
+  };
+  float s = 0.0f;
+#pragma unroll 2
+  for (int i = tid; i < groups; i += NSC_THREADS) {
+    float f[8];
+    int r, c;
+    load_u(i, true, f, r, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(f[e], f[e], s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) red[warp] = s;
+  __syncthreads();
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NSC_THREADS / 32; ++w) s += red[w];
+  const float scale = kNsScale / (sqrtf(s) + cp.eps);
+#pragma unroll 2
+  for (int i = tid; i < groups; i += NSC_THREADS) {      // each thread what it wrote itself
+    float f[8];
+    int r, c;
+    load_u(i, false, f, r, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= scale;
+    if (p.tall) {
+      for (int e = 0; e < 8 && c + e < p.cols; ++e)
+        *reinterpret_cast<__half*>(xs + nsc_at(c + e, r)) = __float2half_rn(f[e]);
+    } else {
+      *reinterpret_cast<uint4*>(xs + nsc_at(r, c)) = pack_half8(f);
+    }
+  }
+
+  // ---------------------------------------------------------- products
+  const uint32_t xa = smem_u32(xs), aa = smem_u32(as), ba = smem_u32(bs);
+  const int q = warp & 3, part = warp >> 2, row = q * 32 + lane;
+  const bool row_ok = row < p.m;
+  const int k16 = ceil_div(p.m, 16);                     // steps of 16 along m
+  uint32_t phase = 0;
+  bool ok = true;
+  uint32_t taddr = 0, tmem_base = 0;
+  // Operands written by every thread -> the tensor core -> the accumulator.
+  auto multiply = [&](auto issue) {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem_base = tmem_slot;
+    taddr = tmem_base + ((uint32_t)(q * 32) << 16);
+    if (tid == 0) {
+      issue();
+      umma_commit(smem_u32(&done_bar));
+    }
+    ok = wait_bounded(smem_u32(&done_bar), phase, abort_flag, p.err, p.timeout_ns, true);
+    phase ^= 1u;
+    ok = __syncthreads_and(ok);
+    tc_fence_after();
+  };
+  // fp16 operands, M = 128; the square products take N = 128.
+  const uint32_t idesc0 = (1u << 4) | ((uint32_t)(NSC_M >> 4) << 24);
+  const uint32_t idesc_sq = idesc0 | ((uint32_t)(NSC_M >> 3) << 17);
+  for (int k = 0; k < cp.steps && ok; ++k) {
+    const float ca = cp.coeffs[3 * k] * kNsScale, cb = cp.coeffs[3 * k + 1], cc = cp.coeffs[3 * k + 2] / kNsScale;
+    multiply([&]() {                                     // A = X X^T
+      for (int b = 0; b < nb; ++b)
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t d = sw128_desc(xa + b * NSC_BLOCK) + (uint64_t)((kk * 32) >> 4);
+          umma_bf16(tmem_base, d, d, idesc_sq, b > 0 || kk > 0);
+        }
+    });
+    if (!ok) break;
+    for (int c0 = part * 32; c0 < p.m; c0 += 128) {
+      uint32_t r[2][16];
+      tmem_ld16x2_wait(taddr + c0, taddr + c0 + 16, r[0], r[1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[j >> 1][(j & 1) * 8 + e]) * (1.0f / kNsScale);
+        *reinterpret_cast<uint4*>(as + nsc_at(row, c0 + 8 * j)) = pack_half8(v);
+      }
+    }
+    multiply([&]() {                                     // B = a I + b A + c A^2
+      for (int kk = 0; kk < k16; ++kk) {
+        const uint64_t d = sw128_desc(aa + (kk >> 2) * NSC_BLOCK) + (uint64_t)(((kk & 3) * 32) >> 4);
+        umma_bf16(tmem_base, d, d, idesc_sq, kk > 0);
+      }
+    });
+    if (!ok) break;
+    for (int c0 = part * 32; c0 < p.m; c0 += 128) {
+      uint32_t r[2][16];
+      tmem_ld16x2_wait(taddr + c0, taddr + c0 + 16, r[0], r[1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 old = *reinterpret_cast<const uint4*>(as + nsc_at(row, c0 + 8 * j));
+        const __half2* h = reinterpret_cast<const __half2*>(&old);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = (e & 1) ? __high2float(h[e >> 1]) : __low2float(h[e >> 1]);
+          v[e] = cb * x + cc * __uint_as_float(r[j >> 1][(j & 1) * 8 + e]);
+          if (c0 + 8 * j + e == row) v[e] += ca;
+        }
+        *reinterpret_cast<uint4*>(bs + nsc_at(row, c0 + 8 * j)) = pack_half8(v);
+      }
+    }
+    multiply([&]() {                                     // X = B X
+      for (int j0 = 0; j0 < p.n; j0 += 256) {
+        const int n = min(256, ceil_div(p.n - j0, 16) * 16);
+        const uint32_t idesc = idesc0 | ((uint32_t)(n >> 3) << 17) | (1u << 16);   // X is MN-major
+        for (int kk = 0; kk < k16; ++kk)
+          umma_bf16(tmem_base + j0, sw128_desc(ba + (kk >> 2) * NSC_BLOCK) + (uint64_t)(((kk & 3) * 32) >> 4),
+                    nsc_mn_desc(xa + (j0 >> 6) * NSC_BLOCK) + (uint64_t)((kk * 2 * 1024) >> 4), idesc, kk > 0);
+      }
+    });
+    if (!ok) break;
+    const bool last = k + 1 == cp.steps;
+    for (int c0 = part * 32; c0 < p.n; c0 += 128) {
+      uint32_t r[2][16];
+      tmem_ld16x2_wait(taddr + c0, taddr + c0 + 16, r[0], r[1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (c0 + 8 * j >= p.n) break;
+        float v[8];
+        const float f = last ? 1.0f / (kNsScale * kNsScale) : 1.0f / kNsScale;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)   // columns past n were not computed
+          v[e] = c0 + 8 * j + e < p.n ? __uint_as_float(r[j >> 1][(j & 1) * 8 + e]) * f : 0.0f;
+        if (!last) *reinterpret_cast<uint4*>(xs + nsc_at(row, c0 + 8 * j)) = pack_half8(v);
+        else if (row_ok) ns_store_last(p, mat, row, c0 + 8 * j, v);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_slot, 512);
+  }
+}
+
 // fp16 [outer][rows][cols] with a row pitch, 128-byte swizzle, box 64 x box_rows.
 bool make_ns_tmap(CUtensorMap* tm, const void* base, long long cols, long long rows, long long outer, long long ld,
                   int box_rows) {
@@ -616,6 +857,16 @@ NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
   return q;
 }
 
+bool ns_on_chip(int m, int n) { return m <= NSC_M && n <= NSC_N; }
+
+template <typename T, bool MOM>
+cudaError_t launch_ns_chip(const NsChipParams& cp, cudaStream_t s) {
+  const cudaError_t e = allow_max_smem<ns_chip_kernel<T, MOM>>();
+  if (e != cudaSuccess) return e;
+  ns_chip_kernel<T, MOM><<<cp.g.n_mat, NSC_THREADS, NSC_SMEM, s>>>(cp);
+  return cudaGetLastError();
+}
+
 template <typename T, bool MOM>
 cudaError_t ns_first_x(const OrthoParams& p, const NsPlan& q, int first, int count, char* ws, bool clear,
                        cudaStream_t s) {
@@ -644,23 +895,18 @@ cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cud
   __half* x[2] = {reinterpret_cast<__half*>(ws + q.x0), reinterpret_cast<__half*>(ws + q.x1)};
   __half *a = reinterpret_cast<__half*>(ws + q.a), *b = reinterpret_cast<__half*>(ws + q.b);
   CUtensorMap xk[2], xn[2], ak, bk;
-  for (int i = 0; i < 2; ++i)
+  const bool chip = ns_on_chip(q.m, q.n);
+  for (int i = 0; i < 2 && !chip; ++i)
     if (!make_ns_tmap(&xk[i], x[i], q.n, q.m, q.batch, q.ld_x, NS_HALF) ||
         !make_ns_tmap(&xn[i], x[i], q.n, q.m, q.batch, q.ld_x, NS_BK))
       return cudaErrorInvalidValue;
-  if (!make_ns_tmap(&ak, a, q.m, q.m, q.batch, q.ld_a, NS_HALF) ||
-      !make_ns_tmap(&bk, b, q.m, q.m, q.batch, q.ld_a, NS_HALF))
+  if (!chip && (!make_ns_tmap(&ak, a, q.m, q.m, q.batch, q.ld_a, NS_HALF) ||
+                !make_ns_tmap(&bk, b, q.m, q.m, q.batch, q.ld_a, NS_HALF)))
     return cudaErrorInvalidValue;
   const size_t size = (size_t)p.rows * p.cols;
   for (int first = 0; first < p.n; first += q.batch) {
     const int count = p.n - first < q.batch ? p.n - first : q.batch;
     const bool f32 = p.dtype == MOE_DTYPE_F32, mom = p.momentum != nullptr;
-    cudaError_t e =
-        f32 ? (mom ? ns_first_x<float, true>(p, q, first, count, ws, first == 0, s)
-                   : ns_first_x<float, false>(p, q, first, count, ws, first == 0, s))
-            : (mom ? ns_first_x<__nv_bfloat16, true>(p, q, first, count, ws, first == 0, s)
-                   : ns_first_x<__nv_bfloat16, false>(p, q, first, count, ws, first == 0, s));
-    if (e != cudaSuccess) return e;
     NsGemmParams g = {};
     g.n_mat = count;
     g.m = q.m; g.n = q.n;
@@ -675,6 +921,29 @@ cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cud
     g.step = p.step;
     g.err = reinterpret_cast<uint32_t*>(ws + q.err);
     g.timeout_ns = kDefaultTimeoutNs;
+    if (chip) {
+      NsChipParams cp = {};
+      cp.g = g;
+      cp.grad = static_cast<const char*>(p.g) + first * size * (f32 ? 4 : 2);
+      cp.mom = mom ? p.momentum + first * size : nullptr;
+      cp.mu = p.mu;
+      cp.eps = p.eps;
+      cp.nesterov = p.nesterov;
+      cp.steps = p.steps;
+      cp.clear_err = first == 0;
+      for (int k = 0; k < 3 * p.steps; ++k) cp.coeffs[k] = p.coeffs[k];
+      const cudaError_t e = f32 ? (mom ? launch_ns_chip<float, true>(cp, s) : launch_ns_chip<float, false>(cp, s))
+                                : (mom ? launch_ns_chip<__nv_bfloat16, true>(cp, s)
+                                       : launch_ns_chip<__nv_bfloat16, false>(cp, s));
+      if (e != cudaSuccess) return e;
+      continue;
+    }
+    cudaError_t e =
+        f32 ? (mom ? ns_first_x<float, true>(p, q, first, count, ws, first == 0, s)
+                   : ns_first_x<float, false>(p, q, first, count, ws, first == 0, s))
+            : (mom ? ns_first_x<__nv_bfloat16, true>(p, q, first, count, ws, first == 0, s)
+                   : ns_first_x<__nv_bfloat16, false>(p, q, first, count, ws, first == 0, s));
+    if (e != cudaSuccess) return e;
     for (int k = 0; k < p.steps; ++k) {
       const int cur = k & 1;
       g.a = p.coeffs[3 * k]; g.b = p.coeffs[3 * k + 1]; g.c = p.coeffs[3 * k + 2];
