@@ -11,6 +11,7 @@ path. If the library is missing or cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import os
 from typing import Optional
 
@@ -875,3 +876,21 @@ class MoEBlock:
         run(make_config(self.cfg, T), x, w["w_router"], w.get("bias"), w["w1"], w["w3"], w["w2"],
             w.get("ws1"), w.get("ws3"), w.get("ws2"), out, self.workspace(T), stream)
         return out
+
+    def step(self, h: torch.Tensor, u: torch.Tensor, norm: NormConfig, w_post=None, gate=None, w_pre=None, h_out=None,
+             u_out=None, stream=None):
+        """One layer of a residual stack: ``(h_out, u_out)`` from the stream h and
+        the block's normalised input u. The block runs on u; its output is
+        normalised by w_post, gated, scaled and added to the stream
+        (``moe_residual_norm``; ``norm`` gives the scales, its T and d are h's),
+        and u_out is the next block's input under w_pre (None without one).
+        ``h_out`` may be h, ``u_out`` may be u."""
+        T, d = h.shape
+        y = self.forward(u, stream=stream)
+        if h_out is None:
+            h_out = torch.empty_like(h)
+        if u_out is None and w_pre is not None:
+            u_out = torch.empty_like(h)
+        cfg = make_norm_config(dataclasses.replace(norm, T=T, d=d, dtype="f32" if h.dtype == torch.float32 else "bf16"))
+        moe_residual_norm(cfg, h, y, w_post, gate, w_pre, h_out, u_out, stream)
+        return h_out, u_out

@@ -225,6 +225,8 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
 
+  // The next launch may take the SMs that this one leaves idle and set up there.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS_STAGES; ++i) {
       mbar_init(smem_u32(&full_bar[i]), 1);
@@ -248,7 +250,6 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   // What the launch before wrote is read only from here on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int tm = ceil_div(p.m, NS_TILE);
   const int per = SYM ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, NS_TILE);
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
 
 // ------------------------------------------------------- norm and first X
 constexpr int NS_NORM_THREADS = 256;
+constexpr int NS_NORM_MAX = 256;                   // blocks a matrix
 
 template <typename T> __device__ __forceinline__ void ns_load8(const T* p, float (&f)[8]);
 template <> __device__ __forceinline__ void ns_load8<float>(const float* p, float (&f)[8]) {
@@ -816,6 +818,7 @@ cudaError_t launch_ns_gemm(const CUtensorMap& tp, const CUtensorMap& tq, const N
 }
 
 constexpr size_t kNsAlign = 256;
+constexpr long long kNsL2Bytes = 64LL << 20;       // of 126 MB: 8 x 2048 x 7168 with momentum 318 -> 230 us
 size_t ns_round(size_t v) { return (v + kNsAlign - 1) / kNsAlign * kNsAlign; }
 
 struct NsPlan {
@@ -840,7 +843,7 @@ NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
   const long long rounds = ceil_div_ll(n_mat > 0 ? n_mat : 1, most);
   q.batch = (int)ceil_div_ll(n_mat > 0 ? n_mat : 1, rounds);
   const long long size = (long long)rows * cols, blocks = ceil_div_ll(size, NS_NORM_THREADS * 8 * 4);
-  q.norm_blocks = (int)(blocks < 256 ? blocks : 256);
+  q.norm_blocks = (int)(blocks < NS_NORM_MAX ? blocks : NS_NORM_MAX);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -871,15 +874,23 @@ template <typename T, bool MOM>
 cudaError_t ns_first_x(const OrthoParams& p, const NsPlan& q, int first, int count, char* ws, bool clear,
                        cudaStream_t s) {
   const long long size = (long long)p.rows * p.cols;
-  const T* g = static_cast<const T*>(p.g) + (size_t)first * size;
-  float* mom = MOM ? p.momentum + (size_t)first * size : nullptr;
-  float* partial = reinterpret_cast<float*>(ws + q.partial);
-  ns_norm_kernel<T, MOM><<<dim3(q.norm_blocks, count), NS_NORM_THREADS, 0, s>>>(
-      g, mom, p.mu, p.nesterov, size, size % 8 == 0, partial, clear ? reinterpret_cast<uint32_t*>(ws + q.err) : nullptr);
   const int col_tiles = ceil_div(p.cols, 64);
-  ns_init_kernel<T, MOM><<<dim3((unsigned)(col_tiles * (long long)ceil_div(p.rows, 64)), count), 256, 0, s>>>(
-      g, mom, p.mu, p.nesterov, p.rows, p.cols, p.cols % 8 == 0, p.rows > p.cols, p.eps, partial, q.norm_blocks,
-      col_tiles, reinterpret_cast<__half*>(ws + q.x0), q.ld_x);
+  // The second pass finds U (gradient and momentum) in L2 if the first has not
+  // gone on too far: both over a few matrices at a time.
+  const long long bytes = size * ((long long)sizeof(T) + (MOM ? 4 : 0));
+  const int few = (int)(kNsL2Bytes / bytes < 1 ? 1 : kNsL2Bytes / bytes < count ? kNsL2Bytes / bytes : count);
+  for (int i = 0; i < count; i += few) {
+    const int n = count - i < few ? count - i : few;
+    const T* g = static_cast<const T*>(p.g) + (size_t)(first + i) * size;
+    float* mom = MOM ? p.momentum + (size_t)(first + i) * size : nullptr;
+    float* partial = reinterpret_cast<float*>(ws + q.partial) + (size_t)i * q.norm_blocks;
+    ns_norm_kernel<T, MOM><<<dim3(q.norm_blocks, n), NS_NORM_THREADS, 0, s>>>(
+        g, mom, p.mu, p.nesterov, size, size % 8 == 0, partial,
+        clear && i == 0 ? reinterpret_cast<uint32_t*>(ws + q.err) : nullptr);
+    ns_init_kernel<T, MOM><<<dim3((unsigned)(col_tiles * (long long)ceil_div(p.rows, 64)), n), 256, 0, s>>>(
+        g, mom, p.mu, p.nesterov, p.rows, p.cols, p.cols % 8 == 0, p.rows > p.cols, p.eps, partial, q.norm_blocks,
+        col_tiles, reinterpret_cast<__half*>(ws + q.x0) + (size_t)i * q.m * q.ld_x, q.ld_x);
+  }
   return cudaGetLastError();
 }
 

@@ -63,7 +63,7 @@ def check(cfg, g, o, coeffs=None, matrices=None):
 
 CASES = [(1, 1, 1), (2, 1, 7), (2, 7, 1), (3, 8, 8), (1, 63, 65), (2, 65, 63), (3, 100, 300), (2, 300, 100),
          (5, 128, 128), (1, 257, 513), (1, 513, 257), (2, 256, 1024), (1, 600, 1999), (1, 1031, 520), (2, 768, 768),
-         (1, 5, 3001)]
+         (1, 5, 3001), (2, 128, 512), (1, 512, 128), (1, 129, 512), (1, 128, 513), (1, 97, 449), (1, 8, 8)]
 
 
 @pytest.mark.parametrize("n,rows,cols", CASES)
