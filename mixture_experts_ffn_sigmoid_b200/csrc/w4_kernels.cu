@@ -690,14 +690,21 @@ template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16*
 // gets a NaN scale, so that it shows (the extremes are taken so that a NaN
 // wins).
 //
-// round(w / scale) is taken from w times the reciprocal, which is off by less
-// than 1e-5 steps (four units of 2^-24 of at most 16); only where that lies
-// within 1e-4 of a half, and for scales near the ends of fp32's range, does
-// the thread divide. Adding 2^23 * 1.5 rounds to an integer in the mantissa,
-// ties to even; 8 more is even and changes no tie. Dividing every weight took
-// three times as long as the kernel's bytes.
+// round(w / scale) without a division per weight. t = w times the reciprocal is
+// off by less than 1e-5 (four units of 2^-24 of at most 16).
+//  - bf16 weights: scale and w have 8 significant bits, so 2 w and (2 k + 1)
+//    scale are multiples of one unit that is at least 2^-10 of scale where w is
+//    near (k + 1/2) scale: t lies on a half or at least 2^-10 from it. Rounded
+//    to a multiple of 2^-12 first, it rounds as the exact quotient does.
+//  - fp32 weights: a thread that meets a t within 1e-4 of a half divides.
+// Scales near the ends of fp32's range divide too. Adding 2^23 * 1.5 rounds to
+// an integer in the mantissa, ties to even; the codes' word is summed from
+// these bits as they are, modulo 2^32, what they have in common taken off at
+// the end. Dividing every weight took three times as long as the kernel's
+// bytes, testing every weight for a tie still 125 us at 16384 x 7168.
 constexpr float kRoundMagic = 12582912.0f;
-constexpr int W4_QUANT_AHEAD = 2;   // vectors a thread loads at once
+constexpr float kRound12 = 3072.0f;   // 1.5 * 2^11: multiples of 2^-12
+constexpr int W4_QUANT_AHEAD = 2;     // vectors a thread loads at once
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -709,6 +716,7 @@ template <typename T, bool ZERO>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ w, long long n8, int lanes_log2,
                                                           uint32_t* __restrict__ q, __nv_bfloat16* __restrict__ scale,
                                                           uint8_t* __restrict__ zero) {
+  constexpr bool BF16 = sizeof(T) == 2;
   const long long stride = (long long)gridDim.x * blockDim.x;
   const long long start = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const int lanes = 1 << lanes_log2;
@@ -739,22 +747,28 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T* __restrict__ 
       const bool finite = hi < INFINITY && neg < INFINITY;
       const __nv_bfloat16 s16 = __float2bfloat16_rn(ZERO ? (hi + neg) * (1.0f / 15.0f) : hi * (1.0f / 7.0f));
       const float s = __bfloat162float(s16), step = s > 0.0f ? s : 1.0f, inv = __fdividef(1.0f, step);
-      const int z = ZERO ? (int)fminf(fmaxf(rintf(neg / step), 0.0f), 15.0f) : 8;
+      const float zf = ZERO ? fminf(fmaxf(rintf(neg / step), 0.0f), 15.0f) : 8.0f;
+      const uint32_t z = (uint32_t)zf;
+      // round(w / step) + z clamped to 0..15; without zero points |w / step| is
+      // at most 7.03 and needs no clamp.
       uint32_t word = 0;
+      bool divide = !(step > 1e-37f && step < 1e37f);
       float far = 0.0f;                                // the farthest from an integer
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = f[k][j] * inv, m = t + kRoundMagic;
-        far = fmaxf(far, fabsf(t - (m - kRoundMagic)));
-        int c = __float_as_int(m) - __float_as_int(kRoundMagic) + z;
-        if (ZERO) c = min(max(c, 0), 15);              // without: |t| <= 7.03, 1 to 15 as it is
-        word |= (uint32_t)(c & 15) << (4 * j);
+      for (int j = 7; j >= 0; --j) {
+        float t = BF16 ? fmaf(f[k][j], inv, kRound12) - kRound12 : f[k][j] * inv;
+        if (!BF16) far = fmaxf(far, fabsf(t - ((t + kRoundMagic) - kRoundMagic)));
+        if (ZERO) t = fminf(fmaxf(t, -zf), 15.0f - zf);
+        word = word * 16u + (uint32_t)__float_as_int(t + kRoundMagic);
       }
-      if (!(far <= 0.4999f) || !(step > 1e-37f && step < 1e37f)) {
+      // sum over j of 16^j (bits of 1.5 * 2^23, less z), modulo 2^32
+      word += z * 0x11111111u - 0x4b400000u * 0x11111111u;
+      if (!BF16) divide |= !(far <= 0.4999f);
+      if (divide) {
         word = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float c = fminf(fmaxf(rintf(f[k][j] / step) + (float)z, 0.0f), 15.0f);
+          const float c = fminf(fmaxf(rintf(f[k][j] / step) + zf, 0.0f), 15.0f);
           word |= (uint32_t)c << (4 * j);
         }
       }
