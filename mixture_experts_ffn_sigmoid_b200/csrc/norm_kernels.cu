@@ -45,6 +45,7 @@ namespace {
 constexpr int kNormMaxThreads = 448;
 constexpr int kNormWideVpt = 5;
 constexpr int kNormMaxStages = 4;
+constexpr int kNormSmem = 216 * 1024;   // of an SM
 
 template <typename T> __device__ __forceinline__ void unpack16(const uint4& v, float (&f)[Vec16<T>::N]);
 template <> __device__ __forceinline__ void unpack16<float>(const uint4& v, float (&f)[4]) {
@@ -110,8 +111,9 @@ __device__ __forceinline__ void block_sum4(float (&v)[4], float* red, int& buf) 
     buf ^= 1;
     if ((lane & 7) == 0) r[(lane >> 3) * 32 + w] = c;   // value lane >> 3 of this warp
     __syncthreads();
-    c = 0.0f;
-    for (int i = lane & 7; i < nw; i += 8) c += r[(lane >> 3) * 32 + i];
+    static_assert(kNormMaxThreads <= 16 * 32, "two sums a lane");
+    const int i = lane & 7;
+    c = (i < nw ? r[(lane >> 3) * 32 + i] : 0.0f) + (i + 8 < nw ? r[(lane >> 3) * 32 + i + 8] : 0.0f);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
   }
@@ -140,17 +142,18 @@ struct RowRing {
           if (!src[a] || (int)threadIdx.x + j * nt >= nv)
             base[((size_t)st * ARRAYS * VPT + a * VPT + j) * nt] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void fetch(const uint4* const (&src)[ARRAYS], int row, bool on, int st) const {
+  // The row whose first vector of this thread is `off` vectors into each array.
+  __device__ __forceinline__ void fetch(const uint4* const (&src)[ARRAYS], size_t off, bool on, int st) const {
     if (on) {
       uint4* to = base + (size_t)st * ARRAYS * VPT * nt;
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int v = (int)threadIdx.x + j * nt;
-        if (v < nv)
+      for (int a = 0; a < ARRAYS; ++a)
+        if (src[a]) {
+          const uint4* from = src[a] + off;
 #pragma unroll
-          for (int a = 0; a < ARRAYS; ++a)
-            if (src[a]) cp_async16(to + (a * VPT + j) * nt, src[a] + (size_t)row * nv + v);
-      }
+          for (int j = 0; j < VPT; ++j)
+            if ((int)threadIdx.x + j * nt < nv) cp_async16(to + (a * VPT + j) * nt, from + j * nt);
+        }
     }
     cp_async_commit();
   }
@@ -210,8 +213,13 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
 
   // Row k of this CTA: rows are dealt in turn, so that CTAs work on neighbours.
   const int rows = p.T > (int)blockIdx.x ? (p.T - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-  auto row_of = [&](int k) { return (int)blockIdx.x + k * (int)gridDim.x; };
-  auto fetch = [&](int k, int st) { ring.fetch(src, row_of(k), k < rows, st); };
+  // Offsets run along: of the row to fetch, of the row at hand.
+  const size_t row_step = (size_t)gridDim.x * nv;
+  size_t off_in = (size_t)blockIdx.x * nv + tid, off = off_in;
+  auto fetch = [&](int k, int st) {
+    ring.fetch(src, off_in, k < rows, st);
+    off_in += row_step;
+  };
   ring.clear(src);
   for (int k = 0; k < stages - 1; ++k) fetch(k, k);
 
@@ -222,9 +230,13 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
   BranchWeight<T, VPT> branch = {static_cast<const uint4*>(p.gate), static_cast<const uint4*>(p.w_post), p.beta,
                                  p.w_offset, nt, nv};
   float wbr[VPT][N];
-  int gate_row = rows > 0 ? row_of(0) / p.gate_tokens : 0;
-  branch.load(rows > 0 ? gate_row : 0);
-  branch.open(wbr);
+  // The row's gate row and its place in it, and a step's part in each.
+  int gate_row = (int)blockIdx.x / p.gate_tokens, in_gate = (int)blockIdx.x - gate_row * p.gate_tokens;
+  const int gate_step = (int)gridDim.x / p.gate_tokens, in_step = (int)gridDim.x - gate_step * p.gate_tokens;
+  if (rows > 0) {
+    branch.load(gate_row);
+    branch.open(wbr);
+  }
   auto sum_y = [&](const uint4* slot) -> float {     // this thread's share of y's squares
     float s = 0.0f;
 #pragma unroll
@@ -244,7 +256,6 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
   }
   int st = 0;
   for (int k = 0; k < rows; ++k) {
-    const int t = row_of(k);
     const int next = st + 1 == stages ? 0 : st + 1;
     fetch(k + stages - 1, st == 0 ? stages - 1 : st - 1);
     cp_async_wait(stages - 1);
@@ -261,11 +272,19 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
         o[j][i] = fmaf(ry, f[i] * wbr[j][i], p.alpha * o[j][i]);
         sh = fmaf(o[j][i], o[j][i], sh);
       }
-      if (has_y && tid + j * nt < nv) h_out[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
+      if (has_y && tid + j * nt < nv) h_out[off + j * nt] = pack16<T>(o[j]);
     }
     const bool more = k + 1 < rows;
-    const int next_gate = more ? row_of(k + 1) / p.gate_tokens : gate_row;
-    if (next_gate != gate_row) branch.load(next_gate);
+    int next_gate = gate_row;
+    if (more && p.gate) {
+      next_gate += gate_step;
+      in_gate += in_step;
+      if (in_gate >= p.gate_tokens) {
+        in_gate -= p.gate_tokens;
+        ++next_gate;
+      }
+      if (next_gate != gate_row) branch.load(next_gate);
+    }
     if (more && post) {
       cp_async_wait(stages - 2);
       s[0] = sum_y(ring.slot(next));
@@ -282,9 +301,10 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) residual_norm_kernel(const
         unpack16<T>(wpre[j], w);
 #pragma unroll
         for (int i = 0; i < N; ++i) o[j][i] *= fmaf(r, w[i], ro);
-        if (tid + j * nt < nv) u[(size_t)t * nv + tid + j * nt] = pack16<T>(o[j]);
+        if (tid + j * nt < nv) u[off + j * nt] = pack16<T>(o[j]);
       }
     }
+    off += row_step;
     if (next_gate != gate_row) {
       gate_row = next_gate;
       branch.open(wbr);
@@ -314,12 +334,19 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   const int t0 = blockIdx.x * rows_per_run, t1 = min(p.T, t0 + rows_per_run);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the reduction may line up
   const int gt = p.gate ? p.gate_tokens : p.T;   // without a gate: one group
-  auto fetch = [&](int t, int st) { ring.fetch(src, t, t < t1, st); };
+  size_t off_in = (size_t)t0 * nv + tid, off = off_in;   // of the row to fetch, of the row at hand
+  auto fetch = [&](bool on, int st) {
+    ring.fetch(src, off_in, on, st);
+    off_in += nv;
+  };
   ring.clear(src);
-  for (int i = 0; i < stages - 1; ++i) fetch(t0 + i, i);
+  for (int i = 0; i < stages - 1; ++i) fetch(t0 + i < t1, i);
 
   float wpre[VPT][N], wbr[VPT][N];               // fp32, offsets and beta in
-  float acc_post[VPT][N], acc_pre[VPT][N], acc_s[VPT][N];
+  float acc_pre[VPT][N], acc_s[VPT][N];
+  // dw_post's sums move on only where a gate row closes: in shared memory,
+  // behind the ring, each thread its own.
+  float4* acc_post = reinterpret_cast<float4*>(ring_mem + (size_t)stages * 4 * VPT * nt) + tid;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     unpack16<T>(pre ? __ldg(static_cast<const uint4*>(p.w_pre) + min(tid + j * nt, nv - 1)) : make_uint4(0, 0, 0, 0),
@@ -327,13 +354,17 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       wpre[j][i] += p.w_offset;
-      acc_post[j][i] = acc_pre[j][i] = acc_s[j][i] = 0.0f;
+      acc_pre[j][i] = acc_s[j][i] = 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) acc_post[(j * (N / 4) + i) * nt] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   BranchWeight<T, VPT> branch = {static_cast<const uint4*>(p.gate), static_cast<const uint4*>(p.w_post), p.beta,
                                  p.w_offset, nt, nv};
+  int grp = t0 / gt, left = gt - (t0 - grp * gt);        // gate row, its tokens from this row on
+  bool begins = left == gt;                              // whether it began in this run
   if (t0 < t1) {
-    branch.load(t0 / gt);
+    branch.load(grp);
     branch.open(wbr);
   }
   // This thread's shares of the sums of h'^2, q h', y^2.
@@ -363,7 +394,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   }
   int st = 0;
   for (int t = t0; t < t1; ++t) {
-    fetch(t + stages - 1 < t1 ? t + stages - 1 : t1, st == 0 ? stages - 1 : st - 1);
+    fetch(t + stages - 1 < t1, st == 0 ? stages - 1 : st - 1);
     cp_async_wait(stages - 1);
     const uint4* slot = ring.slot(st);
     const int next = st + 1 == stages ? 0 : st + 1;
@@ -391,7 +422,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
         float a[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) a[i] = p.alpha * dH[i];
-        static_cast<uint4*>(p.dh)[(size_t)t * nv + tid + j * nt] = pack16<T>(a);
+        static_cast<uint4*>(p.dh)[off + j * nt] = pack16<T>(a);
       }
       unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
@@ -402,8 +433,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       }
     }
     // The last row of its gate row, or of the run: its sums go out below.
-    const int grp = t / gt;
-    const bool ends = (t + 1) % gt == 0 || t + 1 == p.T, close = ends || t + 1 == t1;
+    const bool ends = --left == 0 || t + 1 == p.T, close = ends || t + 1 == t1;
     if (close && t + 1 < t1) branch.load(grp + 1);
     const bool ahead = PIPE && t + 1 < t1;
     if (ahead) {
@@ -420,11 +450,10 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
         unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = fmaf(ry, dm[j][i], -cy * f[i]);
-        if (tid + j * nt < nv) static_cast<uint4*>(p.dy)[(size_t)t * nv + tid + j * nt] = pack16<T>(o);
+        if (tid + j * nt < nv) static_cast<uint4*>(p.dy)[off + j * nt] = pack16<T>(o);
       }
     }
     if (has_y && close) {
-      const bool begins = (long long)grp * gt >= t0;
       float* slot_f = nullptr;
       if (!(begins && ends)) slot_f = p.partial + ((size_t)(begins ? 3 : 2) * gridDim.x + blockIdx.x) * p.d;
 #pragma unroll
@@ -436,11 +465,19 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
         if (p.gate) unpack16<T>(__ldg(static_cast<const uint4*>(p.gate) + (size_t)grp * nv + branch.col(j)), g);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float b = p.beta * acc_s[j][i];
-          acc_post[j][i] = fmaf(b, g[i], acc_post[j][i]);
-          o[i] = b * w[i];
+          o[i] = p.beta * acc_s[j][i];
           acc_s[j][i] = 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          float4& a = acc_post[(j * (N / 4) + i / 4) * nt];
+          a.x = fmaf(o[i], g[i], a.x);
+          a.y = fmaf(o[i + 1], g[i + 1], a.y);
+          a.z = fmaf(o[i + 2], g[i + 2], a.z);
+          a.w = fmaf(o[i + 3], g[i + 3], a.w);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] *= w[i];
         if (p.dgate && tid + j * nt < nv) {
           if (slot_f) {
 #pragma unroll
@@ -454,6 +491,12 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       }
       if (t + 1 < t1) branch.open(wbr);
     }
+    if (left == 0) {
+      ++grp;
+      left = gt;
+      begins = true;
+    }
+    off += nv;
     st = next;
   }
 #pragma unroll
@@ -464,7 +507,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
     for (int i = 0; i < N; i += 4) {
       if (p.dw_post)
         *reinterpret_cast<float4*>(p.partial + (size_t)blockIdx.x * p.d + c + i) =
-            make_float4(acc_post[j][i], acc_post[j][i + 1], acc_post[j][i + 2], acc_post[j][i + 3]);
+            acc_post[(j * (N / 4) + i / 4) * nt];
       if (p.dw_pre)
         *reinterpret_cast<float4*>(p.partial + (size_t)(gridDim.x + blockIdx.x) * p.d + c + i) =
             make_float4(acc_pre[j][i], acc_pre[j][i + 1], acc_pre[j][i + 2], acc_pre[j][i + 3]);
@@ -537,8 +580,8 @@ struct NormShape {
   int vpt, threads, ctas_per_sm, stages, smem;
 };
 // One 16-byte vector a thread where 32 threads cover a row, else two, else
-// five; CTAs fill `per_sm` threads an SM and share 200 KB of ring.
-NormShape norm_shape(int dtype, int d, int arrays, int per_sm) {
+// five; CTAs fill `per_sm` threads an SM and share 216 KB of shared memory.
+NormShape norm_shape(int dtype, int d, int arrays, int per_sm, int more) {   // more: bytes a thread and vector
   const int nv = d / (dtype == MOE_DTYPE_F32 ? 4 : 8);
   NormShape s;
   s.vpt = nv > 2 * kNormMaxThreads ? kNormWideVpt : nv > 32 ? 2 : 1;
@@ -547,11 +590,12 @@ NormShape norm_shape(int dtype, int d, int arrays, int per_sm) {
   if (s.ctas_per_sm > 16) s.ctas_per_sm = 16;
   if (s.ctas_per_sm < 1) s.ctas_per_sm = 1;
   const int row = arrays * s.vpt * s.threads * 16;
-  if (200 * 1024 / s.ctas_per_sm / row < 2) s.ctas_per_sm = 1;
-  s.stages = 200 * 1024 / s.ctas_per_sm / row;
+  more *= s.vpt * s.threads;
+  if (kNormSmem / s.ctas_per_sm - more < 2 * row) s.ctas_per_sm = 1;
+  s.stages = (kNormSmem / s.ctas_per_sm - more) / row;
   if (s.stages > kNormMaxStages) s.stages = kNormMaxStages;
   if (s.stages < 1) s.stages = 1;
-  s.smem = s.stages * row;
+  s.smem = s.stages * row + more;
   return s;
 }
 
@@ -562,13 +606,13 @@ bool norm_width_supported(int dtype, int d) {
 }
 
 int norm_backward_runs(int dtype, int T, int d, int num_sms) {
-  const long long n = (long long)norm_shape(dtype, d, 4, kNormMaxThreads).ctas_per_sm * num_sms;
+  const long long n = (long long)norm_shape(dtype, d, 4, kNormMaxThreads, dtype == MOE_DTYPE_F32 ? 16 : 32).ctas_per_sm * num_sms;
   const int per = ceil_div(T, (int)(n < T ? n : T));
   return ceil_div(T, per);
 }
 
 cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.dtype, p.d, 2, 2 * kNormMaxThreads);
+  const NormShape sh = norm_shape(p.dtype, p.d, 2, 2 * kNormMaxThreads, 0);
   const long long slots = (long long)sh.ctas_per_sm * num_sms;
   const int grid = (int)(slots < p.T ? slots : p.T);
   auto go = [&](auto tag) {
@@ -588,7 +632,7 @@ cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t 
 }
 
 cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.dtype, p.d, 4, kNormMaxThreads);
+  const NormShape sh = norm_shape(p.dtype, p.d, 4, kNormMaxThreads, p.dtype == MOE_DTYPE_F32 ? 16 : 32);
   const int runs = norm_backward_runs(p.dtype, p.T, p.d, num_sms);
   const int per = ceil_div(p.T, runs);
   auto go = [&](auto tag) {
