@@ -33,7 +33,7 @@
 // or 32 rows of W2, with up to 8 NT of the segment's token rows) are dealt to
 // the CTAs in contiguous runs of equal length, so a batch that touches few
 // experts still uses every SM. Within a CTA a run is cut where the token rows
-// change; the chunks (256 k) of each piece's tiles go to the 8 warps in equal
+// change; the chunks (256 k) of each piece's tiles go to its 8 warps in equal
 // contiguous shares. A tile that straddles warps is finished by the one that
 // began it, the others leave their sums in shared memory: no barrier but the
 // two around a piece. Each warp streams its chunks through a ring of its own,
@@ -55,7 +55,7 @@ constexpr int W4_THREADS = W4_WARPS * 32;
 constexpr int W4_CHUNK = 256;                       // k of one ring stage
 constexpr int W4_TILE_BYTES = 16 * W4_CHUNK / 2;    // 16 rows of codes
 constexpr int W4_STAGE_BYTES = 2 * W4_TILE_BYTES;
-constexpr int W4_MAX_STAGES = 3;
+constexpr int W4_STAGES = 2;
 
 // A bounded wait by a whole warp, with one outcome for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* err,
@@ -98,7 +98,6 @@ using W4Entry = int4;
 // token rows in fp16 [rows][x_stride] | -8 or -1 times the groups' sums [K /
 // GROUP][8 NT] | the rows' factors [8 NT] | table.
 struct W4Plan {
-  int stages;
   int rows;                 // token rows of a pass, at most 8 NT
   int x_stride;             // bytes of a token row
   int red, x, xs, f, tab;   // offsets
@@ -122,18 +121,17 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
   constexpr int WROWS = MATS == 2 ? 16 : 32;              // weight rows of a tile
   constexpr int NG = W4_CHUNK / GROUP;                    // groups of a chunk: 2, 4 or 8
   constexpr int PER = GROUP / 32;                         // steps of 32 k in a group
-  constexpr int HELD = NG > 4 ? 2 : 1;                    // scales of a row that a lane loads: 4 lanes share a row's
+  constexpr int SCW = NG / 2, ZW = NG > 4 ? 2 : 1;        // words of a row's scales and zero points in a chunk
   extern __shared__ uint8_t w4_raw[];
   uint8_t* w4_dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(w4_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int warp_n[W4_WARPS];
   __shared__ long long warp_u[W4_WARPS];
-  __shared__ uint64_t full_bar[W4_WARPS][W4_MAX_STAGES];
+  __shared__ uint64_t full_bar[W4_WARPS][W4_STAGES];
   __shared__ uint32_t abort_word;
   __shared__ int bad_word;
   volatile uint32_t* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int stages = plan.stages;
-  const uint8_t* ring = w4_dyn + (size_t)warp * stages * W4_STAGE_BYTES;
+  const uint8_t* ring = w4_dyn + (size_t)warp * W4_STAGES * W4_STAGE_BYTES;
   float4* red = reinterpret_cast<float4*>(w4_dyn + plan.red);
   uint8_t* xp = w4_dyn + plan.x;
   float* xsum = reinterpret_cast<float*>(w4_dyn + plan.xs);
@@ -141,7 +139,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
   W4Entry* tab = reinterpret_cast<W4Entry*>(w4_dyn + plan.tab);
   if (tid == 0) {
     for (int w = 0; w < W4_WARPS; ++w)
-      for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full_bar[w][i]), 1);
+      for (int i = 0; i < W4_STAGES; ++i) mbar_init(smem_u32(&full_bar[w][i]), 1);
     abort_word = 0u;
     bad_word = 0;
     fence_mbar_init();
@@ -252,10 +250,9 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
   const uint16_t* psc[2] = {nullptr, nullptr};       // row g's scales
   const uint8_t* pz[2] = {nullptr, nullptr};         // and zero points, or null
   int pgroups = 0;
-  // Scales and zero points of the last chunk started and of the one before it,
-  // rows g and g + 8, as loaded.
-  uint16_t sc_r[2][2][2][HELD] = {};
-  uint8_t z_r[2][2][2][HELD] = {};
+  // Scales (bf16 pairs) and zero points (bytes) of the last chunk started, rows
+  // g and g + 8 of each tile.
+  uint32_t sc_r[2][2][SCW] = {}, z_r[2][2][ZW] = {};
   auto open_tile = [&]() {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
@@ -267,15 +264,6 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
   };
   const uint32_t ring_s = smem_u32(ring);
   auto issue = [&](int slot) {
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < HELD; ++e) {
-          sc_r[0][a][h][e] = sc_r[1][a][h][e];
-          if (ZERO) z_r[0][a][h][e] = z_r[1][a][h][e];
-        }
     while (pleft == 0) {                             // the next piece in which the warp has a share
       if (!next_piece(pseg, ptile, pw)) return;
       const int from = share(pw, warp);
@@ -293,16 +281,61 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
       if (MATS == 2) tma_load_2d(dst + W4_TILE_BYTES, pw.dense ? &tm1s : &tm1, pc * (W4_CHUNK / 2), y, fb);
       else tma_load_2d(dst + W4_TILE_BYTES, pw.dense ? &tm0s : &tm0, pc * (W4_CHUNK / 2), y + 16, fb);
     }
+    // A row's scales of a chunk are NG neighbours: one load, unless K ends
+    // inside a chunk.
+    const int g0 = pc * NG;
+    const bool whole = pgroups % NG == 0;
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int e = 0; e < HELD; ++e) {
-        const int gi = min(pc * NG + (q & (NG / HELD - 1)) * HELD + e, pgroups - 1);
-        sc_r[1][a][0][e] = __ldg(psc[a] + gi);
-        sc_r[1][a][1][e] = __ldg(psc[a] + gi + 8 * pgroups);
-        if (ZERO) {
-          z_r[1][a][0][e] = pz[a] ? __ldg(pz[a] + gi) : (uint8_t)8;
-          z_r[1][a][1][e] = pz[a] ? __ldg(pz[a] + gi + 8 * pgroups) : (uint8_t)8;
+      for (int h = 0; h < 2; ++h) {
+        const uint16_t* sc = psc[a] + h * 8 * pgroups;
+        const uint8_t* z = ZERO && pz[a] ? pz[a] + h * 8 * pgroups : nullptr;
+        uint32_t* to = sc_r[a][h];
+        uint32_t* tz = z_r[a][h];
+        if (whole) {
+          if (NG == 2) to[0] = __ldg(reinterpret_cast<const uint32_t*>(sc + g0));
+          if (NG == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(sc + g0));
+            to[0] = v.x;
+            to[SCW > 1 ? 1 : 0] = v.y;
+          }
+          if (NG == 8) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(sc + g0));
+            to[0] = v.x;
+            to[SCW > 1 ? 1 : 0] = v.y;
+            to[SCW > 2 ? 2 : 0] = v.z;
+            to[SCW > 2 ? 3 : 0] = v.w;
+          }
+          if (ZERO) {
+            if (!z) {
+#pragma unroll
+              for (int i = 0; i < ZW; ++i) tz[i] = 0x08080808u;
+            } else if (NG == 2) {
+              tz[0] = __ldg(reinterpret_cast<const uint16_t*>(z + g0));
+            } else if (NG == 4) {
+              tz[0] = __ldg(reinterpret_cast<const uint32_t*>(z + g0));
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(z + g0));
+              tz[0] = v.x;
+              tz[ZW - 1] = v.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < SCW; ++i) {
+            const int i0 = min(g0 + 2 * i, pgroups - 1), i1 = min(g0 + 2 * i + 1, pgroups - 1);
+            to[i] = (uint32_t)__ldg(sc + i0) | ((uint32_t)__ldg(sc + i1) << 16);
+          }
+          if (ZERO) {
+#pragma unroll
+            for (int i = 0; i < ZW; ++i) {
+              tz[i] = 0;
+#pragma unroll
+              for (int e = 0; e < 4 && e < NG; ++e)
+                tz[i] |= (z ? (uint32_t)__ldg(z + min(g0 + 4 * i + e, pgroups - 1)) : 8u) << (8 * e);
+            }
+          }
         }
       }
     --pleft;
@@ -312,7 +345,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
       if (pleft) open_tile();
     }
   };
-  for (int i = 0; i < stages - 1; ++i) issue(i);
+  issue(0);
 
   if (p.check && blockIdx.x == gridDim.x - 1) {
     // The last CTA checks the caller's indices for all, before anything could
@@ -332,11 +365,11 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
   if (p.wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ------------------------------------------------------------- token rows
-  // A row of a piece by one warp, or by 2, 4 or 8 where there are as few rows:
+  // A row of a piece by one warp, or by 2 or 4 where there are few rows:
   // its largest magnitude (each of them), then its values, eight k a lane paired
   // as the codes are, and its groups' sums (each a share).
   auto stage_rows = [&](const W4Piece& sg) {
-    const int team = sg.rows > 4 ? 1 : sg.rows > 2 ? 2 : sg.rows > 1 ? 4 : 8;
+    const int team = sg.rows > W4_WARPS / 2 ? 1 : sg.rows > W4_WARPS / 4 ? 2 : 4;
     for (int r = warp / team; r < sg.rows; r += W4_WARPS / team) {
       size_t src = sg.t0 + r;
       if (!sg.dense && p.gather) {
@@ -434,22 +467,17 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[a][t][i] = 0.0f;
     for (int k = from; k < to; ++k) {
-      uint32_t sc[2][HELD];                          // rows g and g + 8
-      float zp[2][HELD][2];
-      const int newest = 3 - stages;                 // 1: two stages, this chunk is the last one started
+      uint32_t sc[2][2][SCW], zp[2][2][ZW];
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int e = 0; e < HELD; ++e) {
-          const uint32_t s0 = newest ? sc_r[1][a][0][e] : sc_r[0][a][0][e];
-          const uint32_t s1 = newest ? sc_r[1][a][1][e] : sc_r[0][a][1][e];
-          sc[a][e] = s0 | (s1 << 16);
-          if (ZERO) {
-            zp[a][e][0] = (float)((newest ? z_r[1][a][0][e] : z_r[0][a][0][e]) & 15);
-            zp[a][e][1] = (float)((newest ? z_r[1][a][1][e] : z_r[0][a][1][e]) & 15);
-          }
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < SCW; ++i) sc[a][h][i] = sc_r[a][h][i];
+#pragma unroll
+          for (int i = 0; i < ZW; ++i) zp[a][h][i] = z_r[a][h][i] & 0x0f0f0f0fu;
         }
-      if (ok) issue(slot == 0 ? stages - 1 : slot - 1);
+      if (ok) issue(slot ^ 1);
       ok = ok && warp_wait(smem_u32(&full_bar[warp][slot]), phase, abort_flag, p.err, p.timeout_ns);
       const uint8_t* st = ring + slot * W4_STAGE_BYTES;
       const uint8_t* xc = xlane + c * (2 * W4_CHUNK);
@@ -467,7 +495,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
           xb[t] = *reinterpret_cast<const uint4*>(xc + (size_t)t * 8 * plan.x_stride + s * 64);
           if (s % PER == 0) xs[t] = *reinterpret_cast<const float2*>(xsc + (s / PER) * (8 * NT) + t * 8);
         }
-        const int sub = s / PER, from_lane = (lane & 28) | (sub / HELD);   // the lane that has the group's scales
+        const int sub = s / PER;                     // the chunk's group that step s belongs to
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
           const uint8_t* w = st + a * W4_TILE_BYTES + get[s];
@@ -477,8 +505,9 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
           const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
           float z0 = 1.0f, z1 = 1.0f;
           if (ZERO && s % PER == 0) {
-            z0 = __shfl_sync(0xffffffffu, zp[a][sub % HELD][0], from_lane);
-            z1 = __shfl_sync(0xffffffffu, zp[a][sub % HELD][1], from_lane);
+            // 2^23 + zero point as a float, its last byte picked from the row's
+            z0 = __uint_as_float(__byte_perm(zp[a][0][sub / 4], 0x4b000000u, 0x7440 + (sub & 3))) - 8388608.0f;
+            z1 = __uint_as_float(__byte_perm(zp[a][1][sub / 4], 0x4b000000u, 0x7440 + (sub & 3))) - 8388608.0f;
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -492,8 +521,9 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
             mma_f16(grp[a][t], a1, xb[t].z, xb[t].w);
           }
           if ((s + 1) % PER == 0) {                  // the group's sum is whole
-            const uint32_t ss = __shfl_sync(0xffffffffu, sc[a][sub % HELD], from_lane);
-            const float s0 = __uint_as_float(ss << 16), s1 = __uint_as_float(ss & 0xffff0000u);
+            const uint32_t w0 = sc[a][0][sub / 2], w1 = sc[a][1][sub / 2];
+            const float s0 = __uint_as_float(sub & 1 ? w0 & 0xffff0000u : w0 << 16);
+            const float s1 = __uint_as_float(sub & 1 ? w1 & 0xffff0000u : w1 << 16);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               if (t > 0 && t * 8 >= sg.rows) break;
@@ -506,7 +536,8 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
         }
       }
       __syncwarp();                                  // every lane has read the stage
-      if (++slot == stages) { slot = 0; phase ^= 1u; }
+      slot ^= 1;
+      if (slot == 0) phase ^= 1u;
       if (++c == sg.nch) {                           // the tile ends
         if (began) {
           finish(m);
@@ -563,9 +594,9 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
   // After a wait that ran out: the copies under way land (or have had two more
   // seconds) before shared memory is freed.
   if (!ok && lane == 0)
-    for (int i = 0; i < stages; ++i)
-      wait_bounded(smem_u32(&full_bar[warp][(slot + i) % stages]), phase ^ (slot + i >= stages ? 1u : 0u), abort_flag,
-                   p.err, p.timeout_ns, false);
+    for (int i = 0; i < W4_STAGES; ++i)
+      wait_bounded(smem_u32(&full_bar[warp][slot ^ i]), phase ^ (slot + i >= W4_STAGES ? 1u : 0u), abort_flag, p.err,
+                   p.timeout_ns, false);
 }
 
 // Codes [rows][K/2] as bytes, 128-byte swizzle, box 128 bytes x 16 rows.
@@ -587,9 +618,10 @@ double w4_touched(const W4GemmParams& p) {
   return p.n_routed * (1.0 - pow(1.0 - 1.0 / p.n_routed, (double)p.max_rows));
 }
 
-constexpr int W4_SMEM = 224 * 1024, W4_SMEM_HALF = 115000;   // of one CTA an SM, of two
+// Shared memory of a CTA that has an SM alone, and of two that share one.
+constexpr int W4_SMEM = 232000, W4_SMEM_HALF = 115000;
 
-int w4_layout(const W4GemmParams& p, int nt, int rows, int stages, W4Plan& l) {
+int w4_layout(const W4GemmParams& p, int nt, int rows, W4Plan& l) {
   const int K = p.n_routed > 0 && p.K > p.K_s ? p.K : (p.dense_rows > 0 && p.K_s > p.K ? p.K_s : p.K);
   const int pad = ceil_div(K, W4_CHUNK) * W4_CHUNK;
   int off = 0;
@@ -598,10 +630,9 @@ int w4_layout(const W4GemmParams& p, int nt, int rows, int stages, W4Plan& l) {
     off += ceil_div(bytes, 128) * 128;
     return o;
   };
-  l.stages = stages;
   l.rows = rows;
   l.x_stride = 2 * pad + 64;                // 64 past a multiple of 128: a pair of rows takes every bank once
-  take(W4_WARPS * stages * W4_STAGE_BYTES);
+  take(W4_WARPS * W4_STAGES * W4_STAGE_BYTES);
   l.red = take(W4_WARPS * 2 * nt * 512);
   l.x = take(rows * l.x_stride);
   l.xs = take(pad / p.group * 8 * nt * 4);
@@ -617,9 +648,10 @@ struct W4Shape {
 
 // Token tiles of eight per pass, and CTAs an SM. More token tiles do more
 // products a weight (1, 1.3 and 2 times the time of one), fewer passes over a
-// segment's weights; token rows that do not fit twice in an SM's shared memory
-// leave one CTA there (1.4 times the time), those that do not fit at all take
-// fewer rows a pass. Routed segments vary about their mean.
+// segment's weights. Token rows that do not fit twice in an SM's shared memory
+// leave one CTA there (1.4 times the time; 12 warps instead of 8 in it gained 2%
+// at 7168-wide rows); those that do not fit at all take fewer rows a pass.
+// Routed segments vary about their mean.
 bool w4_shape(const W4GemmParams& p, W4Shape& best) {
   const double act = w4_touched(p), cost[3] = {1.0, 1.3, 2.0};
   double least = 1e300;
@@ -627,23 +659,17 @@ bool w4_shape(const W4GemmParams& p, W4Shape& best) {
     W4Shape s;
     s.nt = 1 << i;
     int rows = 8 * s.nt;
-    while (rows > 1 && w4_layout(p, s.nt, rows, 2, s.plan) > W4_SMEM) rows /= 2;
+    while (rows > 1 && w4_layout(p, s.nt, rows, s.plan) > W4_SMEM) rows /= 2;
     if (s.nt > 1 && rows < 8 * s.nt) break;
-    s.smem = w4_layout(p, s.nt, rows, 2, s.plan);
+    s.smem = w4_layout(p, s.nt, rows, s.plan);
     if (s.smem > W4_SMEM) break;
     s.ctas = s.smem <= W4_SMEM_HALF ? 2 : 1;
-    W4Plan deep;                            // a third stage where there is room
-    const int n = w4_layout(p, s.nt, rows, W4_MAX_STAGES, deep);
-    if (n <= (s.ctas == 2 ? W4_SMEM_HALF : W4_SMEM)) {
-      s.plan = deep;
-      s.smem = n;
-    }
     double t = (double)p.M_s * p.K_s * ceil_div(p.dense_rows, rows);
     if (act > 0.0) {
       const double mean = p.max_rows / act, passes = (mean + sqrt(mean)) / rows;
       t += act * p.M * p.K * (passes > 1.0 ? passes : 1.0);
     }
-    t *= cost[i] * (s.ctas == 1 ? 1.4 : 1.0);
+    t *= cost[i] * (s.ctas == 2 ? 1.0 : 1.4);
     if (t < least) {
       least = t;
       best = s;
