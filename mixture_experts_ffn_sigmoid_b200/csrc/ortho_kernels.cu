@@ -23,7 +23,12 @@
 // steps end 1.2e-3 (2-norm) from fp64 for a spread spectrum, bf16 operands end
 // 1e-2 from it. X, A and B are stored times 64, so that small entries (1e-4
 // and below in wide matrices) stay above fp16's subnormals; powers of two cost
-// nothing. a I is folded into B: its rounding adds less than X's own.
+// nothing. a I is folded into B. The diagonal of B, near 0.7 where the values
+// have converged, is its largest part, and over few rows its roundings do not
+// average out: for m <= 128 what fp16 leaves of it is kept in fp32 and its
+// product with X added by the epilogue (on chip A's as well). Without that,
+// matrices of 8 to 20 rows ended up to 2.8e-3 from fp64, with it 1.2e-3 (in a
+// fp64 simulation of the roundings, 150 random shapes of up to 100 x 2500).
 //
 // Kernels: one pass over U for its norm (and the momentum), one that writes X
 // in fp16 (transposing through shared memory), then three GEMM launches a step
@@ -101,6 +106,8 @@ struct NsGemmParams {
   float a, b, c;            // kNsPoly
   const __half* a_in;       // kNsPoly: A, read again in the epilogue
   __half* out;              // kNsGram: A, kNsPoly: B, kNsApply: the next X
+  const __half* x_in;       // kNsApply, kNsLast: X, read again where diag is set
+  float* diag;              // what fp16 left of B's diagonal, [n_mat][m], or null
   // kNsLast: the caller's matrices, [n_mat][rows][cols]; tall: out = X^T.
   int tall, rows, cols;
   __nv_bfloat16* o;         // result, or null:
@@ -146,6 +153,15 @@ __device__ __forceinline__ uint4 pack_half8(const float (&v)[8]) {
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// v[at], without indexing registers.
+template <int N>
+__device__ __forceinline__ float ns_pick(const float (&v)[N], int at) {
+  float x = v[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) x = e == at ? v[e] : x;
+  return x;
 }
 
 // Eight columns of a row of the last product into the caller's matrices.
@@ -365,7 +381,24 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
             if (j + e == i) x += p.a * kNsScale;
             v[e] = x;
           }
+          if (p.diag && row_ok && i >= j && i < j + 32) {
+            const float x = ns_pick(v, i - j);
+            p.diag[(size_t)t.mat * p.m + i] = x - __half2float(__float2half_rn(x));
+          }
         } else {
+          if (!SYM && p.diag && row_ok) {
+            const float rest = p.diag[(size_t)t.mat * p.m + i];
+            const __half* xp = p.x_in + ((size_t)t.mat * p.m + i) * p.ld_x + j;
+            uint4 xv[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              xv[k] = j + 8 * k < ncol ? *reinterpret_cast<const uint4*>(xp + 8 * k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const __half2 h = reinterpret_cast<const __half2*>(xv)[e >> 1];
+              v[e] = fmaf(rest, (e & 1) ? __high2float(h) : __low2float(h), v[e]);
+            }
+          }
           const float f = MODE == kNsLast ? 1.0f / (kNsScale * kNsScale) : 1.0f / kNsScale;
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] *= f;
@@ -577,6 +610,7 @@ template <typename T, bool MOM>
 __global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_constant__ NsChipParams cp) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ float red[NSC_THREADS / 32];
+  __shared__ __align__(16) float rest_a[NSC_M], rest_b[NSC_M];         // what fp16 left of the diagonals of A and B
   __shared__ uint64_t done_bar;
   __shared__ uint32_t tmem_slot, abort_word;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -595,6 +629,7 @@ __global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_co
     tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
+  if (tid < NSC_M) rest_a[tid] = 0.0f;
   for (int i = tid; i < (nb + 2 * (NSC_M / 64)) * (NSC_BLOCK / 16); i += NSC_THREADS)   // rows and columns past the matrix
     reinterpret_cast<uint4*>(i < nb * (NSC_BLOCK / 16) ? xs : as - nb * NSC_BLOCK)[i] = make_uint4(0, 0, 0, 0);
 
@@ -716,6 +751,10 @@ __global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_co
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[j >> 1][(j & 1) * 8 + e]) * (1.0f / kNsScale);
+        if (c0 + 8 * j == (row & ~7)) {                  // the diagonal
+          const float x = ns_pick(v, row & 7);
+          rest_a[row] = x - __half2float(__float2half_rn(x));
+        }
         *reinterpret_cast<uint4*>(as + nsc_at(row, c0 + 8 * j)) = pack_half8(v);
       }
     }
@@ -726,6 +765,7 @@ __global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_co
       }
     });
     if (!ok) break;
+    const float rest = rest_a[row], cr = fmaf(cc, rest, cb);
     for (int c0 = part * 32; c0 < p.m; c0 += 128) {
       uint32_t r[2][16];
       tmem_ld16x2_wait(taddr + c0, taddr + c0 + 16, r[0], r[1]);
@@ -733,12 +773,21 @@ __global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_co
       for (int j = 0; j < 4; ++j) {
         const uint4 old = *reinterpret_cast<const uint4*>(as + nsc_at(row, c0 + 8 * j));
         const __half2* h = reinterpret_cast<const __half2*>(&old);
+        // (A + D)^2 = A A + D A + A D + ..., D the diagonal's rest
+        const float4 d0 = *reinterpret_cast<const float4*>(&rest_a[c0 + 8 * j]);
+        const float4 d1 = *reinterpret_cast<const float4*>(&rest_a[c0 + 8 * j + 4]);
+        const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float x = (e & 1) ? __high2float(h[e >> 1]) : __low2float(h[e >> 1]);
-          v[e] = cb * x + cc * __uint_as_float(r[j >> 1][(j & 1) * 8 + e]);
-          if (c0 + 8 * j + e == row) v[e] += ca;
+          v[e] = fmaf(fmaf(cc, d[e], cr), x, cc * __uint_as_float(r[j >> 1][(j & 1) * 8 + e]));
+        }
+        if (c0 + 8 * j == (row & ~7)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += e == (row & 7) ? fmaf(cb, rest, ca) : 0.0f;
+          const float x = ns_pick(v, row & 7);
+          rest_b[row] = x - __half2float(__float2half_rn(x));
         }
         *reinterpret_cast<uint4*>(bs + nsc_at(row, c0 + 8 * j)) = pack_half8(v);
       }
@@ -754,6 +803,7 @@ __global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_co
     });
     if (!ok) break;
     const bool last = k + 1 == cp.steps;
+    const float more = row < p.m ? rest_b[row] : 0.0f;
     for (int c0 = part * 32; c0 < p.n; c0 += 128) {
       uint32_t r[2][16];
       tmem_ld16x2_wait(taddr + c0, taddr + c0 + 16, r[0], r[1]);
@@ -762,9 +812,14 @@ __global__ void __launch_bounds__(NSC_THREADS, 1) ns_chip_kernel(const __grid_co
         if (c0 + 8 * j >= p.n) break;
         float v[8];
         const float f = last ? 1.0f / (kNsScale * kNsScale) : 1.0f / kNsScale;
+        const uint4 old = *reinterpret_cast<const uint4*>(xs + nsc_at(row, c0 + 8 * j));
 #pragma unroll
-        for (int e = 0; e < 8; ++e)   // columns past n were not computed
-          v[e] = c0 + 8 * j + e < p.n ? __uint_as_float(r[j >> 1][(j & 1) * 8 + e]) * f : 0.0f;
+        for (int e = 0; e < 8; ++e) {   // columns past n were not computed
+          const __half2 h = reinterpret_cast<const __half2*>(&old)[e >> 1];
+          const float x = (e & 1) ? __high2float(h) : __low2float(h);
+          v[e] = fmaf(more, x, __uint_as_float(r[j >> 1][(j & 1) * 8 + e])) * f;
+          if (c0 + 8 * j + 8 > p.n && c0 + 8 * j + e >= p.n) v[e] = 0.0f;
+        }
         if (!last) *reinterpret_cast<uint4*>(xs + nsc_at(row, c0 + 8 * j)) = pack_half8(v);
         else if (row_ok) ns_store_last(p, mat, row, c0 + 8 * j, v);
       }
@@ -825,7 +880,7 @@ struct NsPlan {
   int m, n, ld_x, ld_a;
   int batch;                // matrices worked on at once
   int norm_blocks;          // partial sums per matrix
-  size_t err, partial, x0, x1, a, b, total;
+  size_t err, partial, x0, x1, a, b, diag, total;
 };
 
 // A matrix is independent of the others; enough of them run together to give
@@ -856,6 +911,7 @@ NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
   q.x1 = take((size_t)q.batch * q.m * q.ld_x * 2);
   q.a = take((size_t)q.batch * q.m * q.ld_a * 2);
   q.b = take((size_t)q.batch * q.m * q.ld_a * 2);
+  q.diag = take(q.m <= NSC_M ? (size_t)q.batch * q.m * 4 : 0);
   q.total = off;
   return q;
 }
@@ -923,6 +979,7 @@ cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cud
     g.m = q.m; g.n = q.n;
     g.ld_x = q.ld_x; g.ld_a = q.ld_a;
     g.a_in = a;
+    g.diag = q.m <= NSC_M ? reinterpret_cast<float*>(ws + q.diag) : nullptr;
     g.tall = p.rows > p.cols;
     g.rows = p.rows; g.cols = p.cols;
     g.o = p.o ? static_cast<__nv_bfloat16*>(p.o) + first * size : nullptr;
@@ -963,6 +1020,7 @@ cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cud
       g.out = b;
       if ((e = launch_ns_gemm<kNsPoly>(ak, ak, g, num_sms, s)) != cudaSuccess) return e;
       g.out = x[cur ^ 1];
+      g.x_in = x[cur];
       e = k + 1 < p.steps ? launch_ns_gemm<kNsApply>(bk, xn[cur], g, num_sms, s)
                           : launch_ns_gemm<kNsLast>(bk, xn[cur], g, num_sms, s);
       if (e != cudaSuccess) return e;

@@ -89,16 +89,17 @@ def swiglu_rows(x, w1, w3, w2):
 MUON_COEFFS = (3.4445, -4.7750, 2.0315)
 
 
-def newton_schulz(u, coeffs, eps=1e-7, stored=lambda v: v):
+def newton_schulz(u, coeffs, eps=1e-7, stored=lambda v: v, stored_a=None, stored_b=None):
     """X of the Newton-Schulz steps for one matrix u; coeffs [(a, b, c)] per
     step. ``stored`` rounds what an implementation keeps between products (X,
-    A = X X^T and a I + b A + c A^2): the identity gives the exact result."""
+    A = X X^T and a I + b A + c A^2): the identity gives the exact result.
+    stored_a and stored_b take its place for the two products."""
     if u.shape[0] > u.shape[1]:
-        return newton_schulz(u.T, coeffs, eps, stored).T
+        return newton_schulz(u.T, coeffs, eps, stored, stored_a, stored_b).T
     x = stored(u / (np.sqrt((u * u).sum()) + eps))
     for k, (a, b, c) in enumerate(coeffs):
-        g = stored(x @ x.T)
-        x = stored(a * np.eye(len(g)) + b * g + c * (g @ g)) @ x
+        g = (stored_a or stored)(x @ x.T)
+        x = (stored_b or stored)(a * np.eye(len(g)) + b * g + c * (g @ g)) @ x
         if k + 1 < len(coeffs):
             x = stored(x)
     return x
@@ -107,6 +108,11 @@ def newton_schulz(u, coeffs, eps=1e-7, stored=lambda v: v):
 def half_64(v):
     """v rounded to IEEE half precision at 64 times its size."""
     return (v * 64.0).astype(np.float16).astype(np.float64) / 64.0
+
+
+def half_64_off_diagonal(v):
+    """half_64 but for the diagonal, which stays."""
+    return half_64(v) + np.diag(np.diag(v - half_64(v)))
 
 
 def muon_direction(g, momentum, mu, nesterov):

@@ -84,6 +84,31 @@ def test_large_stack_in_groups():
     assert B.ortho_workspace_size(cfg) == B.ortho_workspace_size(OrthoConfig(n=350, rows=16, cols=24))
 
 
+@pytest.mark.parametrize("rows,cols", [(9, 400), (13, 415), (300, 12), (76, 8), (15, 1433), (1723, 16)])
+def test_few_rows_keep_the_diagonals(rows, cols):
+    """Over few rows the roundings of B's diagonal would not average out. The
+    weights of a step from zero, in fp32, are X itself; over 64 matrices its
+    error is that of the same roundings in fp64 with the diagonals whole (A's
+    too up to 512 columns): 64 squares of errors have a mean that is within
+    1.5 of another 64's unless single ones dominate, 1.5 in the error itself."""
+    n = 64
+    cfg = OrthoConfig(n=n, rows=rows, cols=cols, dtype="f32")
+    g = gradients(n, rows, cols, "f32", seed=9)
+    w = torch.zeros(n, rows, cols, device="cuda")
+    B.moe_muon_step(cfg, g, torch.zeros_like(w), w, B.alloc_ortho_workspace(cfg), lr=1.0, mu=0.0, weight_decay=0.0)
+    per = [tuple(float(np.float32(v)) for v in lo.MUON_COEFFS)] * 5
+    got, same = [], []
+    for i in range(n):
+        u = f64(g[i])
+        want = lo.newton_schulz(u, per, float(np.float32(cfg.eps)))
+        whole = lo.half_64_off_diagonal
+        near = lo.newton_schulz(u, per, cfg.eps, lo.half_64, whole if max(rows, cols) <= 512 else None, whole)
+        got.append(np.linalg.norm(-f64(w[i]) - want) / np.linalg.norm(want))
+        same.append(np.linalg.norm(near - want) / np.linalg.norm(want))
+    rms = lambda v: float(np.sqrt(np.mean(np.square(v))))
+    assert rms(got) <= 1.5 * rms(same), (rms(got), rms(same))
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 def test_steps_and_coefficients(steps):
     cfg = OrthoConfig(n=2, rows=200, cols=136, steps=steps)
