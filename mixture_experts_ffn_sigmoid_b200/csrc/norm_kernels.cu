@@ -30,8 +30,16 @@
 // stream's; in the backward the stream's and y's squares, then the branch's);
 // the second of one row and the first of the next share a barrier.
 //
+// Measured, bf16, T = 4096, d = 7168: forward 45 us (235 MB: 5.2 TB/s, 79% of
+// the copy rate; 69% of the issue slots), backward 80 us and 6 for the sums over
+// runs (353 MB: 4.1 TB/s; a row's four vectors a thread and the sums leave 14
+// warps an SM, which issue in 55% of the cycles). fp32, T = 1111, d = 1000:
+// backward 16.8 us, two launches' latency more than their 27 MB. 32 rows of
+// 2048: 3.8 us on the GPU.
+//
 // Weight gradients: in the backward each CTA takes a contiguous run of rows
-// and keeps fp32 sums in registers; the runs' sums are added in run order by a
+// and keeps fp32 sums (dw_pre's and the gate's in registers, dw_post's, which
+// change with the gate row only, in shared memory); the runs' sums are added in run order by a
 // second kernel, so results do not depend on timing. A gate row whose tokens
 // all lie in one run is finished by that run; one that straddles runs goes
 // through the run's head or tail slot (a run holds at most one of each).

@@ -35,13 +35,21 @@
 // of one persistent kernel on CTA pairs: 256 x 256 tiles by M = 256, N = 256
 // cta_group::2 MMAs, each CTA staging 128 rows of P and 128 of Q (32 KB per 64
 // of K, six stages), two accumulators in TMEM so that the epilogue of a tile
-// runs under the next one's MMAs. X is the MN-major operand of B X, so it is
+// runs under the next one's MMAs. Where such tiles would leave SMs idle, a CTA
+// takes a tile of 128 x 128 by itself. X is the MN-major operand of B X, so it is
 // stored once. The last step's epilogue writes the result or the weights.
+//
+// Measured, five steps: 8 x 2048 x 7168 as a Muon step in bf16 3.6 to 4.3 ms with
+// the power cap (3.95 TFLOP: 0.92 to 1.1 PFLOP/s; the products alone run at 1.33,
+// 1.02 and 1.36 PFLOP/s for A, B and X, the two first passes take 317 us for
+// their 2.1 GB); 2 x 14336 x 4096 7.0 to 7.3 ms (1.1 PFLOP/s). Middling matrices
+// are bound by the 15 dependent launches: 4 of 256 x 384 take 122 us.
 //
 // Matrices of up to 128 x 512 (either way round) stay in shared memory from the
 // first read to the last write: one launch, one CTA a matrix (ns_chip_kernel).
 // Their products are too short for launches between them: 8 matrices of 256 x
-// 128 took 97 us in 17 launches.
+// 128 took 97 us in 17 launches, 44 here (2.9 us a product: MMAs, the trip
+// through registers and two barriers).
 #include <cuda_fp16.h>
 
 #include "umma_common.cuh"
@@ -51,7 +59,6 @@ namespace {
 
 constexpr int NS_BK = 64;
 constexpr int NS_HALF = 128;                       // rows of a tile per CTA of the pair
-constexpr int NS_TILE = 2 * NS_HALF;
 constexpr int NS_OP_BYTES = NS_HALF * NS_BK * 2;   // one operand's share of a stage
 constexpr int NS_STAGE_BYTES = 2 * NS_OP_BYTES;
 constexpr int NS_STAGES = 6;
@@ -98,6 +105,23 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint16_t mask) {
       : "memory");
 }
 
+template <bool PAIR>
+__device__ __forceinline__ void ns_load(uint32_t dst, const CUtensorMap* tm, int c0, int c1, int c2, uint32_t bar) {
+  if (PAIR) {
+    tma_load_3d_pair(dst, tm, c0, c1, c2, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void ns_commit(uint64_t* bar, uint16_t mask) {
+  if (PAIR) umma_commit_pair(smem_u32(bar), mask);
+  else umma_commit(smem_u32(bar));
+}
+
 enum NsMode { kNsGram = 0, kNsPoly = 1, kNsApply = 2, kNsLast = 3 };
 
 struct NsGemmParams {
@@ -122,9 +146,9 @@ struct NsTile {
   int mat, i0, j0;          // first row and column of D
 };
 
-template <int MODE>
+template <int MODE, int TILE>
 __device__ __forceinline__ NsTile ns_tile(const NsGemmParams& p, int tile) {
-  const int tm = ceil_div(p.m, NS_TILE);
+  const int tm = ceil_div(p.m, TILE);
   NsTile t;
   if (MODE == kNsGram || MODE == kNsPoly) {      // tiles on and below the diagonal
     const int per = tm * (tm + 1) / 2;
@@ -133,14 +157,14 @@ __device__ __forceinline__ NsTile ns_tile(const NsGemmParams& p, int tile) {
     int i = (int)((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
     while (i * (i + 1) / 2 > r) --i;
     while ((i + 1) * (i + 2) / 2 <= r) ++i;
-    t.i0 = i * NS_TILE;
-    t.j0 = (r - i * (i + 1) / 2) * NS_TILE;
+    t.i0 = i * TILE;
+    t.j0 = (r - i * (i + 1) / 2) * TILE;
   } else {                                        // rows fastest: neighbours share X's columns
-    const int per = tm * ceil_div(p.n, NS_TILE);
+    const int per = tm * ceil_div(p.n, TILE);
     t.mat = tile / per;
     const int r = tile - t.mat * per;
-    t.j0 = (r / tm) * NS_TILE;
-    t.i0 = (r % tm) * NS_TILE;
+    t.j0 = (r / tm) * TILE;
+    t.i0 = (r % tm) * TILE;
   }
   return t;
 }
@@ -221,12 +245,15 @@ __device__ __forceinline__ void ns_store_last(const NsGemmParams& p, int mat, in
 }
 
 // D = P Q^T (kNsGram: P = Q = X; kNsPoly: P = Q = A) or D = P Q with Q read
-// MN-major (kNsApply, kNsLast: P = B, Q = X).
-template <int MODE>
+// MN-major (kNsApply, kNsLast: P = B, Q = X). PAIR: a CTA pair per tile of 256 x
+// 256, else one CTA per tile of 128 x 128.
+template <int MODE, bool PAIR>
 __global__ void __launch_bounds__(NS_THREADS, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const NsGemmParams p) {
   constexpr bool SYM = MODE == kNsGram || MODE == kNsPoly;
+  constexpr int TILE = PAIR ? 2 * NS_HALF : NS_HALF;
+  constexpr uint32_t CTAS = PAIR ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem);
@@ -238,7 +265,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
   volatile uint32_t* abort_flag = tmem_slot + 1;
   uint8_t* ring = smem + 1024;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
   const bool leader = rank == 0;
 
   // The next launch may take the SMs that this one leaves idle and set up there.
@@ -250,7 +277,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&accf_bar[i]), 1);
-      mbar_init(smem_u32(&acce_bar[i]), 2 * NS_EPI_WARPS);
+      mbar_init(smem_u32(&acce_bar[i]), CTAS * NS_EPI_WARPS);
     }
     mbar_init(smem_u32(drain_bar), 1);
     *abort_flag = 0u;
@@ -258,19 +285,26 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     tmap_prefetch(&tmP);
     tmap_prefetch(&tmQ);
   }
-  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), NS_TMEM_COLS);
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), NS_TMEM_COLS);
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), NS_TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();             // both CTAs' barriers exist before either signals the other
+  if (PAIR) cluster_sync_all();   // both CTAs' barriers exist before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   // What the launch before wrote is read only from here on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const int tm = ceil_div(p.m, NS_TILE);
-  const int per = SYM ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, NS_TILE);
+  const int tm = ceil_div(p.m, TILE);
+  const int per = SYM ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, TILE);
   const int total = p.n_mat * per;
-  const int group = blockIdx.x >> 1, ngroups = gridDim.x >> 1;
+  const int group = blockIdx.x / CTAS, ngroups = gridDim.x / CTAS;
   const int nk = ceil_div(MODE == kNsGram ? p.n : p.m, NS_BK);
 
   if (warp == 0 && lane == 0) {
@@ -279,7 +313,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int tile = group; tile < total && ok; tile += ngroups) {
-      const NsTile t = ns_tile<MODE>(p, tile);
+      const NsTile t = ns_tile<MODE, TILE>(p, tile);
       const int pi = t.i0 + (int)rank * NS_HALF, qj = t.j0 + (int)rank * NS_HALF;
       for (int kb = 0; kb < nk; ++kb) {
         if (!wait_bounded(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.err, p.timeout_ns, true)) {
@@ -287,15 +321,15 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
           break;
         }
         const uint32_t fb_local = smem_u32(&full_bar[stage]);
-        const uint32_t fb = map_to_cta(fb_local, 0);
+        const uint32_t fb = PAIR ? map_to_cta(fb_local, 0) : fb_local;
         const uint32_t sp = smem_u32(ring + stage * NS_STAGE_BYTES), sq = sp + NS_OP_BYTES;
-        if (leader) mbar_expect_tx(fb_local, 2 * NS_STAGE_BYTES);   // both CTAs' copies
-        tma_load_3d_pair(sp, &tmP, kb * NS_BK, pi, t.mat, fb);
+        if (leader) mbar_expect_tx(fb_local, CTAS * NS_STAGE_BYTES);   // both CTAs' copies
+        ns_load<PAIR>(sp, &tmP, kb * NS_BK, pi, t.mat, fb);
         if (SYM) {
-          tma_load_3d_pair(sq, &tmQ, kb * NS_BK, qj, t.mat, fb);
+          ns_load<PAIR>(sq, &tmQ, kb * NS_BK, qj, t.mat, fb);
         } else {
-          tma_load_3d_pair(sq, &tmQ, qj, kb * NS_BK, t.mat, fb);
-          tma_load_3d_pair(sq + MN_BOX_BYTES, &tmQ, qj + 64, kb * NS_BK, t.mat, fb);
+          ns_load<PAIR>(sq, &tmQ, qj, kb * NS_BK, t.mat, fb);
+          ns_load<PAIR>(sq + MN_BOX_BYTES, &tmQ, qj + 64, kb * NS_BK, t.mat, fb);
         }
         ++issued;
         if (++stage == NS_STAGES) { stage = 0; phase ^= 1u; }
@@ -312,13 +346,13 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool issued = false, ok = true;
-    // fp16 x fp16 -> fp32, M = N = 256; bit 16: Q is MN-major.
-    const uint32_t idesc = (1u << 4) | ((uint32_t)(NS_TILE >> 3) << 17) | ((uint32_t)(NS_TILE >> 4) << 24) |
+    // fp16 x fp16 -> fp32, M = N = TILE; bit 16: Q is MN-major.
+    const uint32_t idesc = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24) |
                            (SYM ? 0u : 1u << 16);
     for (int tile = group; tile < total && ok; tile += ngroups) {
       if (!wait_bounded(smem_u32(&acce_bar[acc]), acc_phase ^ 1u, abort_flag, p.err, p.timeout_ns, true)) break;
       tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)(acc * NS_TILE);
+      const uint32_t d = tmem_base + (uint32_t)(acc * TILE);
       for (int kb = 0; kb < nk; ++kb) {
         if (!wait_bounded(smem_u32(&full_bar[stage]), phase, abort_flag, p.err, p.timeout_ns, true)) {
           ok = false;
@@ -332,35 +366,36 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
         for (int kk = 0; kk < NS_BK / 16; ++kk) {
           const uint64_t kp = (uint64_t)((kk * 32) >> 4);             // 16 k further along a row
           const uint64_t kq = SYM ? kp : (uint64_t)((kk * 2 * 1024) >> 4);
-          umma_f16_pair(d, pd + kp, qd + kq, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          if (PAIR) umma_f16_pair(d, pd + kp, qd + kq, idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+          else umma_bf16(d, pd + kp, qd + kq, idesc, (kb > 0 || kk > 0) ? 1u : 0u);   // kind::f16: idesc says fp16
         }
         issued = true;
-        umma_commit_pair(smem_u32(&empty_bar[stage]), 0x3);
+        ns_commit<PAIR>(&empty_bar[stage], 0x3);
         if (++stage == NS_STAGES) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
-      umma_commit_pair(smem_u32(&accf_bar[acc]), 0x3);
+      ns_commit<PAIR>(&accf_bar[acc], 0x3);
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
     if (issued) {                 // every MMA completes before TMEM is freed
-      umma_commit_pair(smem_u32(drain_bar), 0x1);
+      ns_commit<PAIR>(drain_bar, 0x1);
       wait_bounded(smem_u32(drain_bar), 0u, abort_flag, p.err, p.timeout_ns, false);
     }
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, cbeg = ((warp - 2) >> 2) * NS_HALF;   // TMEM lane quarter, column half
-    const uint32_t acce0 = map_to_cta(smem_u32(&acce_bar[0]), 0);
+    const int q = warp & 3, cbeg = ((warp - 2) >> 2) * (TILE / 2);   // TMEM lane quarter, column half
+    const uint32_t acce0 = PAIR ? map_to_cta(smem_u32(&acce_bar[0]), 0) : smem_u32(&acce_bar[0]);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = group; tile < total; tile += ngroups) {
-      const NsTile t = ns_tile<MODE>(p, tile);
+      const NsTile t = ns_tile<MODE, TILE>(p, tile);
       const int i = t.i0 + (int)rank * NS_HALF + q * 32 + lane;
       const int j0 = t.j0 + cbeg;
       const int ncol = SYM ? p.m : p.n;
       if (!wait_bounded(smem_u32(&accf_bar[acc]), acc_phase, abort_flag, p.err, p.timeout_ns, true)) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * NS_TILE + cbeg);
-      for (int c0 = 0; c0 < NS_HALF && j0 + c0 < ncol; c0 += 32) {
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * TILE + cbeg);
+      for (int c0 = 0; c0 < TILE / 2 && j0 + c0 < ncol; c0 += 32) {
         uint32_t r[2][16];
         tmem_ld16x2_wait(taddr + c0, taddr + c0 + 16, r[0], r[1]);
         const int j = j0 + c0;
@@ -425,16 +460,21 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acce0 + (uint32_t)acc * 8u);
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_cluster(acce0 + (uint32_t)acc * 8u);
+        else mbar_arrive(acce0 + (uint32_t)acc * 8u);
+      }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
   }
   tc_fence_before();
-  cluster_sync_all();             // the peer's shared memory and TMEM stay live until here
+  if (PAIR) cluster_sync_all();   // the peer's shared memory and TMEM stay live until here
+  else __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, NS_TMEM_COLS);
+    if (PAIR) tmem_dealloc_pair(tmem_base, NS_TMEM_COLS);
+    else tmem_dealloc(tmem_base, NS_TMEM_COLS);
   }
 }
 
@@ -849,31 +889,50 @@ bool make_ns_tmap(CUtensorMap* tm, const void* base, long long cols, long long r
 }
 
 template <int MODE>
-cudaError_t launch_ns_gemm(const CUtensorMap& tp, const CUtensorMap& tq, const NsGemmParams& p, int num_sms,
-                           cudaStream_t s) {
-  const cudaError_t e = allow_max_smem<ns_gemm_kernel<MODE>>();
+long long ns_tiles(const NsGemmParams& p, int tile) {
+  const long long tm = ceil_div(p.m, tile);
+  return p.n_mat * (MODE == kNsGram || MODE == kNsPoly ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, tile));
+}
+
+template <int MODE, bool PAIR>
+cudaError_t launch_ns_tiles(const CUtensorMap& tp, const CUtensorMap& tq, const NsGemmParams& p, int num_sms,
+                            cudaStream_t s) {
+  const cudaError_t e = allow_max_smem<ns_gemm_kernel<MODE, PAIR>>();
   if (e != cudaSuccess) return e;
-  const long long tm = ceil_div(p.m, NS_TILE);
-  const long long tiles = p.n_mat * (MODE == kNsGram || MODE == kNsPoly ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, NS_TILE));
-  const int pairs = num_sms / 2;
+  const long long tiles = ns_tiles<MODE>(p, PAIR ? 2 * NS_HALF : NS_HALF);
+  const int ctas = PAIR ? 2 : 1, slots = num_sms / ctas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs));
+  cfg.gridDim = dim3(ctas * (unsigned)(tiles < slots ? tiles : slots));
   cfg.blockDim = dim3(NS_THREADS);
   cfg.dynamicSmemBytes = NS_SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ns_gemm_kernel<MODE>, tp, tq, p);
+  return cudaLaunchKernelEx(&cfg, ns_gemm_kernel<MODE, PAIR>, tp, tq, p);
+}
+
+// One CTA per 128 x 128 tile where that takes less time, in rounds of tiles:
+// such a round takes 0.6 of one of pairs (half the products, but twice the
+// bytes an operation). Five steps, pairs alone -> single CTAs alone -> by this
+// rule: 2 of 768 x 768 229 -> 162 -> 162 us, 3 of 1024 x 4096 402 -> 429 -> 358,
+// 2048 x 7168 687 -> 782 -> 638, 5 of 2000 x 3500 2080 -> 2389 -> 1863, 4096 x
+// 4096 1220 -> 2286 -> (pairs).
+template <int MODE>
+cudaError_t launch_ns_gemm(const CUtensorMap& tp, const CUtensorMap& tq, const NsGemmParams& p, int num_sms,
+                           cudaStream_t s) {
+  const long long pair = ceil_div_ll(ns_tiles<MODE>(p, 2 * NS_HALF), num_sms / 2);
+  const long long one = ceil_div_ll(ns_tiles<MODE>(p, NS_HALF), num_sms);
+  return 0.6 * one < pair ? launch_ns_tiles<MODE, false>(tp, tq, p, num_sms, s)
+                        : launch_ns_tiles<MODE, true>(tp, tq, p, num_sms, s);
 }
 
 constexpr size_t kNsAlign = 256;
-constexpr long long kNsL2Bytes = 64LL << 20;       // of 126 MB: 8 x 2048 x 7168 with momentum 318 -> 230 us
 size_t ns_round(size_t v) { return (v + kNsAlign - 1) / kNsAlign * kNsAlign; }
 
 struct NsPlan {
@@ -892,7 +951,7 @@ NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
   q.n = rows < cols ? cols : rows;
   q.ld_x = (q.n + 7) / 8 * 8;
   q.ld_a = (q.m + 7) / 8 * 8;
-  const long long t = ceil_div(q.m, NS_TILE), tiles = t * (t + 1) / 2;
+  const long long t = ceil_div(q.m, 2 * NS_HALF), tiles = t * (t + 1) / 2;
   long long most = ceil_div_ll(8LL * (num_sms / 2), tiles);
   if (most > 32768) most = 32768;
   const long long rounds = ceil_div_ll(n_mat > 0 ? n_mat : 1, most);
@@ -931,22 +990,17 @@ cudaError_t ns_first_x(const OrthoParams& p, const NsPlan& q, int first, int cou
                        cudaStream_t s) {
   const long long size = (long long)p.rows * p.cols;
   const int col_tiles = ceil_div(p.cols, 64);
-  // The second pass finds U (gradient and momentum) in L2 if the first has not
-  // gone on too far: both over a few matrices at a time.
-  const long long bytes = size * ((long long)sizeof(T) + (MOM ? 4 : 0));
-  const int few = (int)(kNsL2Bytes / bytes < 1 ? 1 : kNsL2Bytes / bytes < count ? kNsL2Bytes / bytes : count);
-  for (int i = 0; i < count; i += few) {
-    const int n = count - i < few ? count - i : few;
-    const T* g = static_cast<const T*>(p.g) + (size_t)(first + i) * size;
-    float* mom = MOM ? p.momentum + (size_t)(first + i) * size : nullptr;
-    float* partial = reinterpret_cast<float*>(ws + q.partial) + (size_t)i * q.norm_blocks;
-    ns_norm_kernel<T, MOM><<<dim3(q.norm_blocks, n), NS_NORM_THREADS, 0, s>>>(
-        g, mom, p.mu, p.nesterov, size, size % 8 == 0, partial,
-        clear && i == 0 ? reinterpret_cast<uint32_t*>(ws + q.err) : nullptr);
-    ns_init_kernel<T, MOM><<<dim3((unsigned)(col_tiles * (long long)ceil_div(p.rows, 64)), n), 256, 0, s>>>(
-        g, mom, p.mu, p.nesterov, p.rows, p.cols, p.cols % 8 == 0, p.rows > p.cols, p.eps, partial, q.norm_blocks,
-        col_tiles, reinterpret_cast<__half*>(ws + q.x0) + (size_t)i * q.m * q.ld_x, q.ld_x);
-  }
+  // Running both passes over a few matrices at a time, so that the second finds
+  // U in L2, took 60 us more on 8 x 2048 x 7168 with momentum: the launches'
+  // ends cost more than the 700 MB saved.
+  const T* g = static_cast<const T*>(p.g) + (size_t)first * size;
+  float* mom = MOM ? p.momentum + (size_t)first * size : nullptr;
+  float* partial = reinterpret_cast<float*>(ws + q.partial);
+  ns_norm_kernel<T, MOM><<<dim3(q.norm_blocks, count), NS_NORM_THREADS, 0, s>>>(
+      g, mom, p.mu, p.nesterov, size, size % 8 == 0, partial, clear ? reinterpret_cast<uint32_t*>(ws + q.err) : nullptr);
+  ns_init_kernel<T, MOM><<<dim3((unsigned)(col_tiles * (long long)ceil_div(p.rows, 64)), count), 256, 0, s>>>(
+      g, mom, p.mu, p.nesterov, p.rows, p.cols, p.cols % 8 == 0, p.rows > p.cols, p.eps, partial, q.norm_blocks,
+      col_tiles, reinterpret_cast<__half*>(ws + q.x0), q.ld_x);
   return cudaGetLastError();
 }
 
