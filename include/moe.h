@@ -549,7 +549,8 @@ MOE_API moe_status moe_w4_dequantize(int64_t rows, int32_t K, int32_t dtype, int
  * moe_expert_swiglu. Any T is computed; the weights of an expert are read
  * again for every 8 to 32 of its rows, so long batches belong to
  * moe_expert_swiglu. Rows of y_perm that no segment covers are left as they
- * were.
+ * were. A token row with an infinity or NaN gives NaN in its own outputs only.
+ * Outputs are distinct arrays; x and x_shared may be one.
  */
 MOE_API moe_status moe_expert_swiglu_w4(const moe_config* cfg, int32_t group, const void* x,
                                 const int32_t* perm_src, const int32_t* expert_offsets,
@@ -576,7 +577,7 @@ typedef struct {
   int32_t rows, cols;   /* of each, 1..65536, any (odd sizes too)                */
   int32_t dtype;        /* moe_dtype of g                                        */
   int32_t steps;        /* Newton-Schulz steps, 1..64                            */
-  float eps;            /* > 0, added to each matrix's Frobenius norm            */
+  float eps;            /* >= 1e-12, added to each matrix's Frobenius norm       */
 } moe_ortho_config;
 
 /*
@@ -608,6 +609,7 @@ typedef struct {
  *   momentum [n][rows][cols]  fp32 IN/OUT
  *   weight   [n][rows][cols]  weight_dtype IN/OUT, rounded once
  *   lr, mu, weight_decay, scale   finite
+ *   g, momentum and weight are distinct arrays
  *
  * Both: every pointer 16-byte aligned; workspace of
  * moe_ortho_workspace_size(cfg) bytes (0: cfg is not valid). Large stacks are
@@ -675,6 +677,7 @@ MOE_API moe_status moe_residual_norm(const moe_norm_config* cfg, const void* h, 
  *   dy       [T][d]  OUT, NULL: not wanted (or no y); may be du
  *   dw_post  [d], dgate (gate's shape), dw_pre [d]
  *                    OUT, each NULL: not wanted; not NULL only where its input is given
+ *                    All outputs are distinct arrays.
  *
  * The norms' factors are recomputed from h_out and y. Weight and gate
  * gradients are summed over tokens in fp32 in a fixed order (the same bits

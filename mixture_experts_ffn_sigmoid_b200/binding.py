@@ -585,7 +585,12 @@ class W4Matrix:
     """A weight matrix (or stack of them) [..., K] in 4 bits with group scales:
     ``q`` uint8 [..., K/2] (even k in the low four bits), ``scale`` bf16
     [..., K/group], ``zero`` uint8 [..., K/group] or None for 8 everywhere.
-    ``W = scale * (code - zero)``."""
+    ``W = scale * (code - zero)``. The three tensors are the matrix's for its
+    lifetime; their contents may change."""
+
+    q = property(lambda self: self._tensors[0])
+    scale = property(lambda self: self._tensors[1])
+    zero = property(lambda self: self._tensors[2])
 
     def __init__(self, q, scale, zero=None, group: int = 128):
         _need(q, "q", 0, _U8)
@@ -595,10 +600,10 @@ class W4Matrix:
             raise ValueError(f"group {group}: expected 32, 64 or 128")
         if q.dim() < 1 or (2 * q.shape[-1]) % group:
             raise ValueError(f"q: rows of {2 * q.shape[-1] if q.dim() else 0} codes are not whole groups of {group}")
-        self.q, self.scale, self.zero, self.group = q, scale, zero, group
+        self._tensors, self.group = (q, scale, zero), group
         self.K = 2 * q.shape[-1]
         self.rows = q.numel() // q.shape[-1] if q.numel() else 0
-        self._key = None
+        self._struct = self._at = None
         for t, name in ((scale, "scale"), (zero, "zero")):
             if t is not None and t.numel() != self.rows * (self.K // group):
                 raise ValueError(f"{name}: {t.numel()} elements, expected {self.rows * (self.K // group)}")
@@ -621,18 +626,18 @@ class W4Matrix:
         return m
 
     def _c(self):
-        """Reference to the C struct, with the tensors' addresses of now: checked
-        anew when a tensor, its address or the current device is another one."""
-        q, scale, zero = self.q, self.scale, self.zero
-        key = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(), id(q), id(scale), id(zero),
-               torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2)
-        if key != self._key:
+        """Reference to the C struct. The matrix's own tensors are checked when it
+        is first used, and again if one's storage has moved (``tensor.data = ``)
+        or the current device is another."""
+        q, scale, zero = self._tensors
+        at = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
+              torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2)
+        if at != self._at:
             groups = self.rows * (self.K // self.group)
             a = _args((q, "q", self.rows * (self.K // 2), _U8, True), (scale, "scale", groups, torch.bfloat16, True),
                       (zero, "zero", groups, _U8, False))
-            self._struct = CW4Matrix(*a)
-            self._ref, self._key = ctypes.byref(self._struct), key
-        return self._ref
+            self._struct, self._at = CW4Matrix(*a), at
+        return ctypes.byref(self._struct)
 
 
 def _dense_code(w, name: str) -> int:
@@ -707,15 +712,12 @@ def moe_forward_w4(cfg, x, w_router, bias, w1, w3, w2, ws1, ws3, ws2, y, workspa
     """The block on 4-bit expert weights (W4Matrix); the router's weights are bf16."""
     c = _cfg(cfg)
     dt = _dt(c)
-    _need(x, "x", c.T * c.d, dt)
-    _need(w_router, "w_router", c.E * c.d, dt)
-    _need(bias, "bias", c.E, _F32, required=False)
-    _need(y, "y", c.T * c.d, dt)
-    _need_ws(workspace)
     group, (a1, a3, a2, s1, s3, s2) = _w4_args(c, w1, w3, w2, ws1, ws3, ws2)
-    px, pr, pb, py, pw = _ptrs(x, w_router, bias, y, workspace)
+    px, pr, pb, py, pw = _args((x, "x", c.T * c.d, dt, True), (w_router, "w_router", c.E * c.d, dt, True),
+                               (bias, "bias", c.E, _F32, False), (y, "y", c.T * c.d, dt, True),
+                               (workspace, "workspace", 1, _U8, True))
     _check(lib().moe_forward_w4(ctypes.byref(c), group, px, pr, pb, a1, a3, a2, s1, s3, s2, py, pw,
-                                workspace.numel(), _stream(stream)), "moe_forward_w4")
+                                workspace.numel(), _raw_stream(stream)), "moe_forward_w4")
 
 
 # --------------------------------------------------------- orthogonalisation

@@ -758,7 +758,9 @@ moe_status check_ortho_config(const moe_ortho_config* c) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->n < 0 || c->rows <= 0 || c->cols <= 0 || c->steps < 1 || c->steps > 64) return MOE_ERR_INVALID_ARG;
   if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
-  if (!(c->eps > 0.0f) || !isfinite(c->eps)) return MOE_ERR_INVALID_ARG;
+  // Below 1e-12 a norm whose squares are lost to fp32's smallest numbers could
+  // count against eps.
+  if (!(c->eps >= 1e-12f) || !isfinite(c->eps)) return MOE_ERR_INVALID_ARG;
   return c->rows > 65536 || c->cols > 65536 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
@@ -1416,6 +1418,7 @@ moe_status moe_orthogonalize(const moe_ortho_config* cfg, const float* coeffs, c
   if (c.n == 0) return MOE_OK;
   MOE_TRY(need(g));
   MOE_TRY(need(o));
+  if (o == g && c.dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
   OrthoParams p = {};
   p.n = c.n; p.rows = c.rows; p.cols = c.cols; p.dtype = c.dtype; p.steps = c.steps;
   p.eps = c.eps;
@@ -1442,6 +1445,7 @@ moe_status moe_muon_step(const moe_ortho_config* cfg, const float* coeffs, const
   MOE_TRY(need(g));
   MOE_TRY(need(momentum));
   MOE_TRY(need(weight));
+  if (g == momentum || g == weight || momentum == weight) return MOE_ERR_INVALID_ARG;
   OrthoParams p = {};
   p.n = c.n; p.rows = c.rows; p.cols = c.cols; p.dtype = c.dtype; p.steps = c.steps;
   p.eps = c.eps;
@@ -1501,6 +1505,7 @@ moe_status moe_expert_swiglu_w4(const moe_config* cfg, int32_t group, const void
   if (c.f_shared > 0) {
     MOE_TRY(need(x_shared));
     MOE_TRY(need(y_shared));
+    if (y_shared == y_perm) return MOE_ERR_INVALID_ARG;
   }
   return enqueue_experts_w4(c, group, x, perm_src, expert_offsets, w1, w3, w2, x_shared, ws1, ws3, ws2, y_perm,
                             y_shared, workspace, false, static_cast<cudaStream_t>(stream));
@@ -1594,7 +1599,10 @@ moe_status moe_residual_norm_backward(const moe_norm_config* cfg, const void* h_
   if (w_pre) MOE_TRY(need(h_out));
   for (const void* q : {y, w_post, gate, w_pre, du, dh_out}) MOE_TRY(maybe(q));
   for (const void* q : {(const void*)dh, (const void*)dy, (const void*)dgate}) MOE_TRY(maybe(q));
-  if (dh && dh == dy) return MOE_ERR_INVALID_ARG;
+  const void* outs[] = {dh, dy, dw_post, dgate, dw_pre};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (outs[i] && outs[i] == outs[j]) return MOE_ERR_INVALID_ARG;
   NormBwdParams p = {c.dtype, c.T, c.d, c.gate_tokens, c.eps, y ? c.alpha : 1.0f, c.beta, c.w_offset,
                      w_pre ? h_out : nullptr, y, w_post, gate, w_pre, du, dh_out, dh, dy, dw_post, dgate, dw_pre,
                      static_cast<float*>(workspace)};

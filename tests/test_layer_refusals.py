@@ -77,6 +77,13 @@ def test_norm_backward_pointers(kw, status):
     assert B.lib().moe_residual_norm_backward(ctypes.byref(c), *[a[n] for n in NAMES], BIG, None) == status
 
 
+@pytest.mark.parametrize("one,other", [("dw_post", "dw_pre"), ("dgate", "dy"), ("dgate", "dh"), ("dh", "dw_pre"), ("dgate", "dw_post")])
+def test_norm_backward_outputs_are_distinct(one, other):
+    a = {n: FAKE + 4096 * i for i, n in enumerate(NAMES)}
+    a[one] = a[other]
+    assert B.lib().moe_residual_norm_backward(ctypes.byref(norm()), *[a[n] for n in NAMES], BIG, None) == B.MOE_ERR_INVALID_ARG
+
+
 def test_norm_backward_workspace_must_be_large_enough():
     c = norm()
     need = B.norm_backward_workspace_size(c)
@@ -175,6 +182,10 @@ def test_w4_expert_tables(kw, status):
     assert call_experts_w4(moe_cfg(), **kw) == status
 
 
+def test_w4_outputs_are_distinct():
+    assert call_experts_w4(moe_cfg(), y=FAKE + 4096, ys=FAKE + 4096) == B.MOE_ERR_INVALID_ARG
+
+
 def test_w4_no_tokens():
     assert call_experts_w4(moe_cfg(T=0), x=None, y=None) == B.MOE_OK
     assert call_forward_w4(moe_cfg(T=0), x=None, y=None) == B.MOE_OK
@@ -200,6 +211,13 @@ def test_w4_matrix_binding():
         B.moe_w4_quantize(torch.zeros(3, 128), m)
     with pytest.raises(ValueError, match="dtype"):
         B.moe_w4_dequantize(m, torch.zeros(4, 128, dtype=torch.float16))
+
+
+def test_w4_matrix_keeps_its_tensors():
+    m = B.W4Matrix.empty(4, 128, group=64, device="cpu")
+    for name in ("q", "scale", "zero"):
+        with pytest.raises(AttributeError):
+            setattr(m, name, None)
 
 
 def test_w4_block_binding():
@@ -258,6 +276,20 @@ def test_ortho_pointers_and_workspace():
     assert need > 0 and call_ortho(c, n=need - 1) == B.MOE_ERR_WORKSPACE_TOO_SMALL
     assert call_muon(c, n=need - 1) == B.MOE_ERR_WORKSPACE_TOO_SMALL
     assert call_ortho(ortho(n=0), g=None, o=None) == B.MOE_OK
+
+
+def test_ortho_arrays_that_must_be_distinct():
+    f32, bad = ortho(dtype="f32"), B.MOE_ERR_INVALID_ARG
+    assert call_ortho(f32, g=FAKE, o=FAKE) == bad            # o is half as wide: a matrix's result in another's gradient
+    a, b = FAKE + 4096, FAKE + 8192
+    for kw in (dict(g=a, m=a, w=b), dict(g=a, m=b, w=a), dict(g=b, m=a, w=a)):
+        assert call_muon(f32, **kw) == bad
+
+
+def test_ortho_eps_below_what_fp32_squares_hold():
+    for eps in (1e-13, 1e-30):
+        assert B.ortho_workspace_size(ortho(eps=eps)) == 0 and call_ortho(ortho(eps=eps)) == B.MOE_ERR_INVALID_ARG
+    assert B.ortho_workspace_size(ortho(eps=1e-11)) > 0
 
 
 @pytest.mark.parametrize("abc,ok", [
