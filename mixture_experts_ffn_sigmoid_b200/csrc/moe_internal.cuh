@@ -267,6 +267,9 @@ struct W4GemmParams {
   void* out;                // [max_rows][M]
   int dense_rows, M_s, K_s; // the shared expert, 0 rows: none
   const void* x_s; void* out_s;
+  // The intermediate is a pair of bf16 values: what the first leaves, in arrays
+  // of the same shape (mats = 2: written, mats = 1: read).
+  const void *x_lo, *x_s_lo; void *out_lo, *out_s_lo;
   W4Operand w[2], w_s[2];
   int has_zero;             // some operand has zero points
   int check;                // check offsets and gather, and write the error word anew

@@ -48,7 +48,7 @@
 // Matrices of up to 128 x 512 (either way round) stay in shared memory from the
 // first read to the last write: one launch, one CTA a matrix (ns_chip_kernel).
 // Their products are too short for launches between them: 8 matrices of 256 x
-// 128 took 97 us in 17 launches, 44 here (2.9 us a product: MMAs, the trip
+// 128 took 97 us in 17 launches, 45 here (2.9 us a product: MMAs, the trip
 // through registers and two barriers).
 #include <cuda_fp16.h>
 

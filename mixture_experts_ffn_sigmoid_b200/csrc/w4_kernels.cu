@@ -24,7 +24,10 @@
 // Token rows as fp16: a row is scaled by the power of two that brings its
 // largest magnitude into [2^14, 2^15), the k under the 0x00f0 masks by 1/16
 // besides. fp16's eleven bits hold bf16's eight; only values below 2^-27 of
-// the row's largest lose bits. A CTA makes them in shared memory when it comes
+// the row's largest lose bits. The intermediate h goes from the first launch to
+// the second as a pair of bf16 values, so that it loses bits only there (2^-11):
+// as one bf16 value it made the result's error 1.4 times its own rounding, up to
+// 1.6 times for narrow experts. A CTA makes them in shared memory when it comes
 // to a segment, with each group's sum, off which the zero points come: it is
 // where the group's product starts from. The product takes its scale in fp32.
 // No weight is rounded.
@@ -43,7 +46,7 @@
 // tiles) is 5 shared reads, 20 integer instructions and 4 products.
 //
 // Measured: 32 tokens, 128 experts of 768 x 2048, top 8 (273 MB of weights and
-// rows): 56.6 us the two launches in one stream, 4.8 TB/s, 74% of the copy
+// rows): 60 us the two launches in one stream, 4.5 TB/s, 69% of the copy
 // rate; gate/up alone 39.9 us with half of the issue slots taken and the
 // integer pipe at 54%. 1 token: 16.4 us, most of it two launches' start and the
 // first loads. 24 tokens, 32 experts of 2048 x 7168 and the shared one, groups
@@ -386,6 +389,10 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
       }
       const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s : p.x) +
                                                         src * (size_t)sg.K);
+      const uint4* row_lo =
+          MATS == 1 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s_lo : p.x_lo) +
+                                                     src * (size_t)sg.K)
+                    : nullptr;
       const int n8 = sg.K / 8;
       uint32_t big = 0;                                  // bf16 magnitudes order like their bits, NaN above infinity
 #pragma unroll 8
@@ -418,6 +425,17 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
           x[2 * j] = __uint_as_float(w[j] << 16) * f1 * f2;
           x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * f1 * f2;
         }
+        if (MATS == 1) {       // the pair, rounded to fp16 for the products and their sum alike
+          const uint4 l = i < n8 ? row_lo[i] : make_uint4(0, 0, 0, 0);
+          const uint32_t wl[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 h = __half22float2(__floats2half2_rn(x[2 * j] + __uint_as_float(wl[j] << 16) * f1 * f2,
+                                                              x[2 * j + 1] + __uint_as_float(wl[j] & 0xffff0000u) * f1 * f2));
+            x[2 * j] = h.x;
+            x[2 * j + 1] = h.y;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += x[j];
         *reinterpret_cast<uint4*>(to + i * 16) =
@@ -447,7 +465,9 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
     float acc[2][NT][4];
     // A finished tile: lane's rows g and g + 8, token columns 2 q and 2 q + 1.
     auto finish = [&](int m) {
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sg.dense ? p.out_s : p.out) + (size_t)sg.t0 * sg.M + m + g;
+      const size_t first = (size_t)sg.t0 * sg.M + m + g;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sg.dense ? p.out_s : p.out) + first;
+      __nv_bfloat16* out_lo = MATS == 2 ? static_cast<__nv_bfloat16*>(sg.dense ? p.out_s_lo : p.out_lo) + first : nullptr;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -457,10 +477,11 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
           const float2 fac = xfac[n];
           const float v0 = acc[0][t][i] * fac.x * fac.y, v1 = acc[1][t][i] * fac.x * fac.y;
           __nv_bfloat16* at = out + (size_t)n * sg.M + (i >> 1) * 8;
-          // One rounding, of the activation (gate/up) or of the result (down).
-          if (MATS == 2) {
-            at[0] = __float2bfloat16_rn(v0 / (1.0f + __expf(-v0)) * v1);
-          } else {
+          if (MATS == 2) {     // the activation as a pair: bf16 alone would double the result's error
+            const float v = v0 / (1.0f + __expf(-v0)) * v1;
+            at[0] = __float2bfloat16_rn(v);
+            out_lo[(size_t)n * sg.M + (i >> 1) * 8] = __float2bfloat16_rn(v - __bfloat162float(at[0]));
+          } else {             // the result's one rounding
             at[0] = __float2bfloat16_rn(v0);
             at[16] = __float2bfloat16_rn(v1);
           }

@@ -184,6 +184,27 @@ def test_experts(T, d, E, k, f, fs, group, zeros):
     check_experts(*a, *run_experts(*a))
 
 
+@pytest.mark.parametrize("T,d,f,fs", [(1, 2048, 32, 32), (2, 1024, 64, 0), (9, 2048, 32, 128)])
+def test_the_intermediate_adds_little_to_the_result_s_rounding(T, d, f, fs):
+    """A narrow expert's row can rest on one intermediate value, whose rounding
+    then moves all of it: by at most fp16's half step, 2^-11 of it (bf16's would
+    be 2^-8). Rounding the result leaves an rms error of 0.42 2^-8 (mantissas
+    spread over a binade), so the first is at most r = 2^-3 / 0.42 = 0.30 of it.
+    Over d >= 1024 values the two errors' correlation c is within 4 / sqrt(d) =
+    0.125 (four sigma): together sqrt(1 + r^2 + 2 r c) = 1.08 at most; fp32's
+    2^-15 disappears beside that."""
+    cfg, x, w, ws, perm_src, offsets = make(T, d, 4, 2, f, fs, 32, True, seed=11)
+    y, ys = run_experts(cfg, x, w, ws, perm_src, offsets)
+    off, xp = offsets.tolist(), f64(x)[perm_src.cpu().numpy()]
+    for e in range(4):
+        if off[e] < off[e + 1]:
+            want = lo.swiglu_rows(xp[off[e]:off[e + 1]], *[dense(m, e) for m in w])[0]
+            got = f64(y[off[e]:off[e + 1]])
+            once = f64(torch.from_numpy(want).to(BF))
+            for i in range(len(want)):
+                assert np.linalg.norm(got[i] - want[i]) <= 1.08 * np.linalg.norm(once[i] - want[i])
+
+
 @pytest.mark.parametrize("T,skew", [(20, 1.0), (70, 1.0)])
 def test_experts_on_skewed_routing_and_packed_rows(T, skew):
     # Every token takes experts 0 and 1, the others have no rows.
