@@ -269,19 +269,26 @@ def _ptrs(*tensors):
     return out
 
 
+_Tensor = torch.Tensor
+
+
 def _args(*specs):
     """Addresses of (tensor, name, least elements, dtype, required) in order.
     One pass over tensors that are as they should be (a decode step makes many
     small calls); anything else goes through _need and _ptrs for its error."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    dev = None
     out = []
     for t, _, n, dt, required in specs:
         if t is None:
             if required and n > 0:
                 break
             out.append(None)
-        elif isinstance(t, torch.Tensor) and t.dtype is dt and t.numel() >= n and t.get_device() == dev \
-                and t.is_contiguous():
+        elif isinstance(t, _Tensor) and t.dtype is dt and t.numel() >= n and t.is_contiguous():
+            on = t.get_device()
+            if on != dev:                  # the first: on the current device (below 0: on the host)
+                if dev is not None or on < 0 or on != torch._C._cuda_getDevice():
+                    break
+                dev = on
             out.append(t.data_ptr())
         else:
             break
@@ -603,7 +610,7 @@ class W4Matrix:
         self._tensors, self.group = (q, scale, zero), group
         self.K = 2 * q.shape[-1]
         self.rows = q.numel() // q.shape[-1] if q.numel() else 0
-        self._struct = self._at = None
+        self._struct = self._ref = self._at = None
         for t, name in ((scale, "scale"), (zero, "zero")):
             if t is not None and t.numel() != self.rows * (self.K // group):
                 raise ValueError(f"{name}: {t.numel()} elements, expected {self.rows * (self.K // group)}")
@@ -630,14 +637,15 @@ class W4Matrix:
         is first used, and again if one's storage has moved (``tensor.data = ``)
         or the current device is another."""
         q, scale, zero = self._tensors
-        at = (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
-              torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2)
-        if at != self._at:
+        at = self._at
+        if at is None or at != (q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
+                                torch._C._cuda_getDevice()):
             groups = self.rows * (self.K // self.group)
             a = _args((q, "q", self.rows * (self.K // 2), _U8, True), (scale, "scale", groups, torch.bfloat16, True),
                       (zero, "zero", groups, _U8, False))
-            self._struct, self._at = CW4Matrix(*a), at
-        return ctypes.byref(self._struct)
+            self._struct = CW4Matrix(*a)
+            self._ref, self._at = ctypes.byref(self._struct), (*a, torch._C._cuda_getDevice())
+        return self._ref
 
 
 def _dense_code(w, name: str) -> int:

@@ -392,7 +392,9 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
       const int i = t.i0 + (int)rank * NS_HALF + q * 32 + lane;
       const int j0 = t.j0 + cbeg;
       const int ncol = SYM ? p.m : p.n;
-      if (!wait_bounded(smem_u32(&accf_bar[acc]), acc_phase, abort_flag, p.err, p.timeout_ns, true)) break;
+      // One outcome for the warp, whose lanes load TMEM together.
+      if (!__all_sync(0xffffffffu, wait_bounded(smem_u32(&accf_bar[acc]), acc_phase, abort_flag, p.err, p.timeout_ns, true)))
+        break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * TILE + cbeg);
       for (int c0 = 0; c0 < TILE / 2 && j0 + c0 < ncol; c0 += 32) {

@@ -158,6 +158,10 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
     if (MATS == 2) tmap_prefetch(&tm1);
   }
 
+  // What the launches before wrote, the routing among it, gate/up reads only from
+  // here on; down waits below, after its first weights.
+  if (!p.wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");
+
   // -------------------------------------------------- the segments' table
   const int n_seg = p.n_routed + (p.dense_rows > 0 ? 1 : 0);
   int base_n = 0;
@@ -206,10 +210,12 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
     }
     __syncthreads();
   }
+  // Down may start beside gate/up from here on: the routing that it reads too is
+  // complete. (Down itself does not call the next launch in early: waiting CTAs
+  // in its SMs cost the wide case 7%.)
+  if (!p.wait_previous) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // A count past 32 bits comes from overlapping segments, a bad table: no work.
   const int n_act = base_n, total = base_u <= 0x7fffffffLL ? (int)base_u : 0;
-  if (!p.wait_previous) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   // A CTA's share of the chunks, moved down to where tiles begin: positions
   // are (segment, tile), a segment's tiles counted pass after pass.
   auto seg_chunks = [&](int s) { return ceil_div(s >= p.n_routed ? p.K_s : p.K, W4_CHUNK); };
@@ -889,7 +895,7 @@ cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = p.wait_previous ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, tm[0], tm[1], tm[2], tm[3], p, shape.plan);
   };
   auto with = [&](auto mats, auto n, auto zero) {
