@@ -14,7 +14,8 @@
 //
 // What bounds it: the tensor cores. A step is 2 m^2 n + 2 m^3 + 2 m^2 n
 // operations; A and A^2 are symmetric, so the tiles above the diagonal are
-// not computed but written from those below: 3 m^2 n + m^3.
+// not computed but written from those below (where SMs would idle otherwise, they
+// are computed): 3 m^2 n + m^3.
 //
 // Precision. The operands are fp16, accumulated in fp32 in TMEM, and rounded
 // once per product. X starts with norm 1 and its singular values stay in a
@@ -43,7 +44,10 @@
 // the power cap (3.95 TFLOP: 0.92 to 1.1 PFLOP/s; the products alone run at 1.33,
 // 1.02 and 1.36 PFLOP/s for A, B and X, the two first passes take 317 us for
 // their 2.1 GB); 2 x 14336 x 4096 7.0 to 7.3 ms (1.1 PFLOP/s). Middling matrices
-// are bound by the 15 dependent launches: 4 of 256 x 384 take 122 us.
+// are bound by their 15 dependent products: 4 of 256 x 384 take 94 us, of which a
+// product's loads (196 KB a tile at an SM's 65 bytes a cycle), its way out of TMEM
+// and the stores' way to the next one are 1.5 to 2 us each. One launch for all
+// products with waits across the grid in between took longer (122 -> 147 us).
 //
 // Matrices of up to 128 x 512 (either way round) stay in shared memory from the
 // first read to the last write: one launch, one CTA a matrix (ns_chip_kernel).
@@ -132,6 +136,7 @@ struct NsGemmParams {
   __half* out;              // kNsGram: A, kNsPoly: B, kNsApply: the next X
   const __half* x_in;       // kNsApply, kNsLast: X, read again where diag is set
   float* diag;              // what fp16 left of B's diagonal, [n_mat][m], or null
+  int full;                 // kNsGram, kNsPoly: all tiles, none mirrored
   // kNsLast: the caller's matrices, [n_mat][rows][cols]; tall: out = X^T.
   int tall, rows, cols;
   __nv_bfloat16* o;         // result, or null:
@@ -150,7 +155,7 @@ template <int MODE, int TILE>
 __device__ __forceinline__ NsTile ns_tile(const NsGemmParams& p, int tile) {
   const int tm = ceil_div(p.m, TILE);
   NsTile t;
-  if (MODE == kNsGram || MODE == kNsPoly) {      // tiles on and below the diagonal
+  if ((MODE == kNsGram || MODE == kNsPoly) && !p.full) {   // tiles on and below the diagonal
     const int per = tm * (tm + 1) / 2;
     t.mat = tile / per;
     const int r = tile - t.mat * per;
@@ -160,7 +165,7 @@ __device__ __forceinline__ NsTile ns_tile(const NsGemmParams& p, int tile) {
     t.i0 = i * TILE;
     t.j0 = (r - i * (i + 1) / 2) * TILE;
   } else {                                        // rows fastest: neighbours share X's columns
-    const int per = tm * ceil_div(p.n, TILE);
+    const int per = tm * (MODE == kNsGram || MODE == kNsPoly ? tm : ceil_div(p.n, TILE));
     t.mat = tile / per;
     const int r = tile - t.mat * per;
     t.j0 = (r / tm) * TILE;
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int tm = ceil_div(p.m, TILE);
-  const int per = SYM ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, TILE);
+  const int per = SYM ? (p.full ? tm * tm : tm * (tm + 1) / 2) : tm * ceil_div(p.n, TILE);
   const int total = p.n_mat * per;
   const int group = blockIdx.x / CTAS, ngroups = gridDim.x / CTAS;
   const int nk = ceil_div(MODE == kNsGram ? p.n : p.m, NS_BK);
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(NS_THREADS, 1)
             *reinterpret_cast<uint4*>(p.out + ((size_t)t.mat * p.m + i) * ld + j + 8 * k) = pack_half8(w);
           }
         }
-        if (SYM && t.i0 != t.j0 && row_ok) {   // the tile above the diagonal: consecutive lanes, consecutive columns
+        if (SYM && !p.full && t.i0 != t.j0 && row_ok) {   // the tile above the diagonal: consecutive lanes, consecutive columns
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (j + e < ncol) p.out[((size_t)t.mat * p.m + j + e) * p.ld_a + i] = __float2half_rn(v[e]);
@@ -893,16 +898,28 @@ bool make_ns_tmap(CUtensorMap* tm, const void* base, long long cols, long long r
 template <int MODE>
 long long ns_tiles(const NsGemmParams& p, int tile) {
   const long long tm = ceil_div(p.m, tile);
-  return p.n_mat * (MODE == kNsGram || MODE == kNsPoly ? tm * (tm + 1) / 2 : tm * ceil_div(p.n, tile));
+  if (MODE == kNsGram || MODE == kNsPoly) return p.n_mat * (p.full ? tm * tm : tm * (tm + 1) / 2);
+  return p.n_mat * tm * ceil_div(p.n, tile);
 }
 
 template <int MODE, bool PAIR>
-cudaError_t launch_ns_tiles(const CUtensorMap& tp, const CUtensorMap& tq, const NsGemmParams& p, int num_sms,
+cudaError_t launch_ns_tiles(const CUtensorMap& tp, const CUtensorMap& tq, NsGemmParams p, int num_sms,
                             cudaStream_t s) {
   const cudaError_t e = allow_max_smem<ns_gemm_kernel<MODE, PAIR>>();
   if (e != cudaSuccess) return e;
-  const long long tiles = ns_tiles<MODE>(p, PAIR ? 2 * NS_HALF : NS_HALF);
+  constexpr int TILE = PAIR ? 2 * NS_HALF : NS_HALF;
   const int ctas = PAIR ? 2 : 1, slots = num_sms / ctas;
+  long long tiles = ns_tiles<MODE>(p, TILE);
+  if (MODE == kNsGram || MODE == kNsPoly) {
+    // Where all tiles take no more rounds than those on and below the diagonal,
+    // nothing is mirrored: the stores of a tile's transpose (2 bytes a lane) are
+    // a quarter of a short product. 4 of 256 x 384 122 -> 94 us, 2 of 768 x 768
+    // 163 -> 136.
+    p.full = 1;
+    const long long all = ns_tiles<MODE>(p, TILE);
+    if (ceil_div_ll(all, slots) <= ceil_div_ll(tiles, slots)) tiles = all;
+    else p.full = 0;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas * (unsigned)(tiles < slots ? tiles : slots));
   cfg.blockDim = dim3(NS_THREADS);
@@ -924,7 +941,7 @@ cudaError_t launch_ns_tiles(const CUtensorMap& tp, const CUtensorMap& tq, const 
 // bytes an operation). Five steps, pairs alone -> single CTAs alone -> by this
 // rule: 2 of 768 x 768 229 -> 162 -> 162 us, 3 of 1024 x 4096 402 -> 429 -> 358,
 // 2048 x 7168 687 -> 782 -> 638, 5 of 2000 x 3500 2080 -> 2389 -> 1863, 4096 x
-// 4096 1220 -> 2286 -> (pairs).
+// 4096 1220 -> 2286 -> (pairs). (Squares with mirrored tiles everywhere.)
 template <int MODE>
 cudaError_t launch_ns_gemm(const CUtensorMap& tp, const CUtensorMap& tq, const NsGemmParams& p, int num_sms,
                            cudaStream_t s) {

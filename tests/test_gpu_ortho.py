@@ -74,6 +74,15 @@ def test_orthogonalize(n, rows, cols, dtype):
     check(cfg, g, run(cfg, g))
 
 
+@pytest.mark.parametrize("n,rows,cols", [(3, 1024, 1100), (8, 700, 720), (4, 640, 777), (60, 130, 140), (2, 1500, 1300)])
+def test_every_way_of_tiling(n, rows, cols):
+    # Squares by 128 x 128 tiles with and without mirrored ones, by pairs'
+    # 256 x 256, and X's products by either.
+    cfg = OrthoConfig(n=n, rows=rows, cols=cols)
+    g = gradients(n, rows, cols, "bf16", seed=6)
+    check(cfg, g, run(cfg, g), matrices=[0, n - 1])
+
+
 def test_large_stack_in_groups():
     # 8 tiles of each of 74 pairs are one group: the stack takes two.
     cfg = OrthoConfig(n=700, rows=16, cols=24)
