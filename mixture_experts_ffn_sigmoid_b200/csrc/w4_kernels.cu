@@ -46,11 +46,11 @@
 // tiles) is 5 shared reads, 20 integer instructions and 4 products.
 //
 // Measured: 32 tokens, 128 experts of 768 x 2048, top 8 (273 MB of weights and
-// rows): 60 us the two launches in one stream, 4.5 TB/s, 69% of the copy
+// rows): 58 us the two launches in one stream, 4.7 TB/s, 72% of the copy
 // rate; gate/up alone 39.9 us with half of the issue slots taken and the
-// integer pipe at 54%. 1 token: 16.4 us, most of it two launches' start and the
+// integer pipe at 54%. 1 token: 16.6 us, most of it two launches' start and the
 // first loads. 24 tokens, 32 experts of 2048 x 7168 and the shared one, groups
-// of 64 with zero points (797 MB): 297 us, 2.7 TB/s: its token rows (115 KB)
+// of 64 with zero points (797 MB): 302 us, 2.6 TB/s: its token rows (115 KB)
 // leave one CTA an SM, whose 8 warps issue in 46% of the cycles.
 #include <cuda_fp16.h>
 
