@@ -43,10 +43,10 @@
 // Measured, five steps: 8 x 2048 x 7168 as a Muon step in bf16 3.6 to 4.3 ms with
 // the power cap (3.95 TFLOP: 0.92 to 1.1 PFLOP/s; the products alone run at 1.33,
 // 1.02 and 1.36 PFLOP/s for A, B and X, the two first passes take 317 us for
-// their 2.1 GB); 2 x 14336 x 4096 7.0 to 7.3 ms (1.1 PFLOP/s). Middling matrices
+// their 2.1 GB); 2 x 14336 x 4096 6.9 to 7.4 ms (1.1 PFLOP/s). Middling matrices
 // are bound by their 15 dependent products: 4 of 256 x 384 take 94 us, of which a
-// product's loads (196 KB a tile at an SM's 65 bytes a cycle), its way out of TMEM
-// and the stores' way to the next one are 1.5 to 2 us each. One launch for all
+// product's loads, its way out of TMEM and the stores' way to the next one are
+// 1.5 to 2 us each. One launch for all
 // products with waits across the grid in between took longer (122 -> 147 us).
 //
 // Matrices of up to 128 x 512 (either way round) stay in shared memory from the
