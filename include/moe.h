@@ -657,8 +657,11 @@ typedef struct {
  *   u       [T][d]   OUT (NULL exactly if w_pre is); may be y, or h if h_out is not
  *
  * Sums are fp32; h_out and u are each rounded once (u from the unrounded
- * stream). Squares are taken in fp32, so a value past 1.8e19 makes its row's
- * mean infinite. Arrays overlap only where named. T = 0 enqueues nothing.
+ * stream). Squares are summed in fp32: a row whose sum of squares passes 3.4e38
+ * (one value of 1.8e19, or an RMS of 1.8e19 / sqrt(d)) has an infinite mean and
+ * the norm 0. Up to there, and for any eps that is a normal number, the results
+ * and the gradients are as good as elsewhere. Arrays overlap only where named.
+ * T = 0 enqueues nothing.
  */
 MOE_API moe_status moe_residual_norm(const moe_norm_config* cfg, const void* h, const void* y,
                              const void* w_post, const void* gate, const void* w_pre, void* h_out,

@@ -412,7 +412,9 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       block_sum4(s, red, buf);
     }
     const float rh = pre ? rsqrtf(s[0] * inv_d + p.eps) : 0.0f, ry = post ? rsqrtf(s[2] * inv_d + p.eps) : 1.0f;
-    const float ch = rh * rh * rh * s[1] * inv_d;
+    // r mean(q n), formed so that nothing leaves fp32's range before the result
+    // does: r^3 by itself is lost past an RMS of 1e13 and infinite below 1e-13.
+    const float ch = rh * (rh * s[1] * inv_d);
     float dm[VPT][N], sy = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -422,9 +424,8 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       unpack16<T>(ring.get(slot, 2, j), q);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float qr = q[i] * rh;
-        acc_pre[j][i] = fmaf(qr, f[i], acc_pre[j][i]);
-        dH[i] = fmaf(-ch, f[i], fmaf(qr, wpre[j][i], dH[i]));
+        acc_pre[j][i] = fmaf(q[i] * rh, f[i], acc_pre[j][i]);
+        dH[i] = fmaf(rh, fmaf(-ch, f[i], q[i] * wpre[j][i]), dH[i]);
       }
       if (p.dh && tid + j * nt < nv) {
         float a[N];
@@ -451,13 +452,13 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
     s[3] = sy;
     if (ahead || post) block_sum4(s, red, buf);
     if (p.dy) {
-      const float cy = post ? ry * ry * ry * s[3] * inv_d : 0.0f;
+      const float cy = post ? ry * (ry * s[3] * inv_d) : 0.0f;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         float f[N], o[N];
         unpack16<T>(ring.get(slot, 1, j), f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(ry, dm[j][i], -cy * f[i]);
+        for (int i = 0; i < N; ++i) o[i] = ry * fmaf(-cy, f[i], dm[j][i]);
         if (tid + j * nt < nv) static_cast<uint4*>(p.dy)[off + j * nt] = pack16<T>(o);
       }
     }
