@@ -10,6 +10,7 @@ path. If the library is missing or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -307,6 +308,18 @@ def _raw_stream(stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocating_on(stream):
+    """Context in which torch allocates memory of ``stream`` (None: the current
+    stream, a Stream or a raw handle). The allocator hands a tensor's memory on
+    in the order of the stream it was allocated on, so what kernels on another
+    one write or read could still be, or already be again, someone else's."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream))
+    return torch.cuda.stream(stream)
 
 
 def _check(status: int, where: str):
@@ -627,8 +640,9 @@ class W4Matrix:
 
     @classmethod
     def quantize(cls, w: torch.Tensor, group: int = 128, zero_points: bool = False, stream=None) -> "W4Matrix":
-        """The 4-bit form of a dense bf16 or fp32 matrix (stack)."""
-        m = cls.empty(*w.shape, group=group, zero_points=zero_points, device=w.device)
+        """The 4-bit form of a dense bf16 or fp32 matrix (stack), in memory of ``stream``."""
+        with _allocating_on(stream):
+            m = cls.empty(*w.shape, group=group, zero_points=zero_points, device=w.device)
         moe_w4_quantize(w, m, stream)
         return m
 
@@ -864,6 +878,11 @@ class MoEBlock:
     ``forward(x)`` returns a new ``[T, d]`` tensor (shared + routed, no
     residual) computed by ``moe_forward``, or by ``moe_forward_w4`` where the
     expert weights are ``W4Matrix``.
+
+    Calls run on ``stream`` (None: the current one), which comes after the work
+    that makes their inputs; tensors that they return are allocated on it. Calls
+    of one T share a workspace: they belong on one stream, or are ordered by
+    events.
     """
 
     def __init__(self, cfg: MoEConfig, weights: dict, device="cuda"):
@@ -872,19 +891,21 @@ class MoEBlock:
         self.device = torch.device(device)
         self._ws = {}
 
-    def workspace(self, T: int) -> torch.Tensor:
+    def workspace(self, T: int, stream=None) -> torch.Tensor:
         if T not in self._ws:
-            self._ws[T] = alloc_workspace(make_config(self.cfg, T), self.device)
+            with _allocating_on(stream):
+                self._ws[T] = alloc_workspace(make_config(self.cfg, T), self.device)
         return self._ws[T]
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         T = x.shape[0]
         if out is None:
-            out = torch.empty_like(x)
+            with _allocating_on(stream):
+                out = torch.empty_like(x)
         w = self.w
         run = moe_forward_w4 if isinstance(w["w1"], W4Matrix) else moe_forward
         run(make_config(self.cfg, T), x, w["w_router"], w.get("bias"), w["w1"], w["w3"], w["w2"],
-            w.get("ws1"), w.get("ws3"), w.get("ws2"), out, self.workspace(T), stream)
+            w.get("ws1"), w.get("ws3"), w.get("ws2"), out, self.workspace(T, stream), stream)
         return out
 
     def step(self, h: torch.Tensor, u: torch.Tensor, norm: NormConfig, w_post=None, gate=None, w_pre=None, h_out=None,
@@ -897,10 +918,11 @@ class MoEBlock:
         ``h_out`` may be h, ``u_out`` may be u."""
         T, d = h.shape
         y = self.forward(u, stream=stream)
-        if h_out is None:
-            h_out = torch.empty_like(h)
-        if u_out is None and w_pre is not None:
-            u_out = torch.empty_like(h)
+        with _allocating_on(stream):
+            if h_out is None:
+                h_out = torch.empty_like(h)
+            if u_out is None and w_pre is not None:
+                u_out = torch.empty_like(h)
         cfg = make_norm_config(dataclasses.replace(norm, T=T, d=d, dtype="f32" if h.dtype == torch.float32 else "bf16"))
         moe_residual_norm(cfg, h, y, w_post, gate, w_pre, h_out, u_out, stream)
         return h_out, u_out
