@@ -339,7 +339,9 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   const RowRing<4, VPT> ring = {ring_mem + tid, nt, nv, stages};
   const float inv_d = 1.0f / (float)p.d;
   int buf = 0;
-  const int t0 = blockIdx.x * rows_per_run, t1 = min(p.T, t0 + rows_per_run);
+  // T may be the largest int: nothing is added to a token's number before it is
+  // known to stay below T.
+  const int t0 = blockIdx.x * rows_per_run, t1 = t0 + min(p.T - t0, rows_per_run);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the reduction may line up
   const int gt = p.gate ? p.gate_tokens : p.T;   // without a gate: one group
   size_t off_in = (size_t)t0 * nv + tid, off = off_in;   // of the row to fetch, of the row at hand
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
     off_in += nv;
   };
   ring.clear(src);
-  for (int i = 0; i < stages - 1; ++i) fetch(t0 + i < t1, i);
+  for (int i = 0; i < stages - 1; ++i) fetch(i < t1 - t0, i);
 
   float wpre[VPT][N], wbr[VPT][N];               // fp32, offsets and beta in
   float acc_pre[VPT][N], acc_s[VPT][N];
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
   }
   int st = 0;
   for (int t = t0; t < t1; ++t) {
-    fetch(t + stages - 1 < t1, st == 0 ? stages - 1 : st - 1);
+    fetch(stages - 1 < t1 - t, st == 0 ? stages - 1 : st - 1);
     cp_async_wait(stages - 1);
     const uint4* slot = ring.slot(st);
     const int next = st + 1 == stages ? 0 : st + 1;
@@ -616,8 +618,8 @@ bool norm_width_supported(int dtype, int d) {
 
 int norm_backward_runs(int dtype, int T, int d, int num_sms) {
   const long long n = (long long)norm_shape(dtype, d, 4, kNormMaxThreads, dtype == MOE_DTYPE_F32 ? 16 : 32).ctas_per_sm * num_sms;
-  const int per = ceil_div(T, (int)(n < T ? n : T));
-  return ceil_div(T, per);
+  const long long per = ceil_div_ll(T, n < T ? n : T);
+  return (int)ceil_div_ll(T, per);
 }
 
 cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t s) {
@@ -643,7 +645,7 @@ cudaError_t launch_residual_norm(const NormParams& p, int num_sms, cudaStream_t 
 cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, cudaStream_t s) {
   const NormShape sh = norm_shape(p.dtype, p.d, 4, kNormMaxThreads, p.dtype == MOE_DTYPE_F32 ? 16 : 32);
   const int runs = norm_backward_runs(p.dtype, p.T, p.d, num_sms);
-  const int per = ceil_div(p.T, runs);
+  const int per = (int)ceil_div_ll(p.T, runs);
   auto go = [&](auto tag) {
     constexpr auto kernel = decltype(tag)::value;
     const cudaError_t e = allow_max_smem<kernel>();
@@ -661,7 +663,7 @@ cudaError_t launch_residual_norm_backward(const NormBwdParams& p, int num_sms, c
   const cudaError_t e = p.dtype == MOE_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
   if (e != cudaSuccess || !(p.dw_post || p.dw_pre || p.dgate)) return e;
   // No gate row straddles runs of whole gate rows.
-  const int gates = ceil_div(p.T, p.gate_tokens < p.T ? p.gate_tokens : p.T), by_run = gates > runs - 1;
+  const int gates = (int)ceil_div_ll(p.T, p.gate_tokens), by_run = gates > runs - 1;
   const int straddle = !p.dgate || per % p.gate_tokens == 0 ? 0 : by_run ? runs - 1 : gates;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ceil_div(p.d, 128), 2 + straddle);

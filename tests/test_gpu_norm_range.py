@@ -47,3 +47,50 @@ def test_zero_and_small_rows_under_a_small_eps(T, d, dtype, eps):
     assert (h_out[2] == 0).all() and (u[2] == 0).all()
     N.check_forward(cfg, dt, t, h_out, u)
     N.check_backward(cfg, dt, t, du, dh, h_out, N.backward(cfg, dt, t, du, dh, h_out))
+
+
+@pytest.fixture
+def freed():
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,gt", [(2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 30 + 5), (2 ** 30 + 77, 2 ** 30 + 76)])
+def test_as_many_tokens_as_an_int_counts(T, gt, freed):
+    """The first and last tokens, those around the gate rows' border and those
+    around a run's; every other gradient is zero, so that the sums are of a few
+    terms each and the bounds those of a small batch."""
+    d = 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    at = sorted({0, 1, 518217, 518218, T // 2, gt - 1, min(gt, T - 1), T - 4, T - 2, T - 1})
+    gates = -(-T // gt)
+    cfg, small = N.NormConfig(T=T, d=d, gate_tokens=gt), N.NormConfig(T=len(at), d=d, gate_tokens=1)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    hs, ys, dus, gate, wp, wn = rn(len(at), d), rn(len(at), d), rn(len(at), d), rn(gates, d), 1 + 0.2 * rn(d), 1 + 0.2 * rn(d)
+    rows = torch.tensor(at, device="cuda")
+    h, y = torch.zeros(T, d, device="cuda", dtype=torch.bfloat16), torch.zeros(T, d, device="cuda", dtype=torch.bfloat16)
+    h[rows], y[rows] = hs, ys
+    # A gate row a token, repeated, in place of rows shared by 2^30 tokens.
+    rep = gate[rows // gt].contiguous()
+    t = dict(h=hs, y=ys, w_post=wp, gate=rep, w_pre=wn)
+    h1, u1 = N.forward(small, torch.bfloat16, t)
+    want = N.backward(small, torch.bfloat16, t, dus, None, h1)
+    B = N.B
+    B.moe_residual_norm(cfg, h, y, wp, gate, wn, h, y)                  # in place: u over y
+    assert torch.equal(h[rows], h1) and torch.equal(y[rows], u1)
+    y.zero_()
+    y[rows] = ys
+    du = torch.zeros(T, d, device="cuda", dtype=torch.bfloat16)
+    du[rows] = dus
+    dwp, dg, dwn = torch.empty_like(wp), torch.empty_like(gate), torch.empty_like(wn)
+    B.moe_residual_norm_backward(cfg, h, y, wp, gate, wn, du, None, None, du, dwp, dg, dwn,
+                                 B.alloc_norm_backward_workspace(cfg))
+    assert torch.equal(du[rows], want["dy"])                            # a row by itself
+    # Each sum once more in its run's order: 10 terms, and the rounding to bf16.
+    near = lambda a, b: (a.double() - b.double()).abs() <= 2 ** -8 * (a.double().abs() + b.double().abs()) + 1e-30
+    assert near(dwp, want["dw_post"]).all() and near(dwn, want["dw_pre"]).all()
+    by_gate = torch.zeros(gates, d, device="cuda", dtype=torch.float64).index_add_(0, rows // gt, want["dgate"].double())
+    room = torch.zeros(gates, d, device="cuda", dtype=torch.float64).index_add_(0, rows // gt, want["dgate"].double().abs())
+    # Each token's part was rounded to bf16 above, and the sum is here, off by 2^-8 of what it came to.
+    assert ((dg.double() - by_gate).abs() <= 2 ** -8 * (room + by_gate.abs() + 2 ** -8 * room) + 1e-30).all()
