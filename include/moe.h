@@ -545,9 +545,10 @@ MOE_API moe_status moe_w4_dequantize(int64_t rows, int32_t K, int32_t dtype, int
  *   y_perm         [T*k][d] bf16 OUT, y_shared [T][d] bf16 OUT (NULL if f_shared == 0)
  *
  * bf16 rows only, d, f and f_shared multiples of group and at most 16384, else
- * MOE_ERR_UNSUPPORTED. The SwiGLU intermediate is kept to more bits than bf16 has
- * (fp16's eleven enter the second product). Any T is computed; the weights of an expert are read
- * again for every 8 to 32 of its rows, so long batches belong to
+ * MOE_ERR_UNSUPPORTED. The SwiGLU intermediate has fp16's eleven significant bits
+ * under a power of two for every eight neighbours (those below 2^-14 of the
+ * largest of the eight lose some). Any T is computed; the weights of an expert
+ * are read again for every 8 to 32 of its rows, so long batches belong to
  * moe_expert_swiglu. Rows of y_perm that no segment covers are left as they
  * were. A token row with an infinity or NaN gives NaN in its own outputs only.
  * Outputs are distinct arrays; x and x_shared may be one.

@@ -79,9 +79,7 @@ Layout layout_of(const moe_config& c) {
   L.offsets = take((E + 1) * 4);
   L.inv_row = take(T * k * 4);
   L.perm_src = take(T * k * 4);
-  // x_perm, or the low halves of the 4-bit experts' intermediate.
-  const size_t lo = c.dtype == MOE_DTYPE_BF16 ? T * (k * f + fs) : 0;
-  L.x_perm = take((T * k * d > lo ? T * k * d : lo) * es);
+  L.x_perm = take(T * k * d * es);
   L.h = take(T * k * f * es);
   L.h_s = take(T * fs * es);
   L.y_perm = take(T * k * d * es);
@@ -856,14 +854,12 @@ moe_status enqueue_experts_w4(const moe_config& c, int group, const void* x, con
   g.M = c.f; g.K = c.d;
   g.x = x; g.gather = perm_src; g.gather_rows = c.T;
   g.out = at<char>(ws, L.h);
-  g.out_lo = at<char>(ws, L.x_perm);
   g.w[0] = w4_operand(w1);
   g.w[1] = w4_operand(w3);
   if (shared) {
     g.dense_rows = c.T; g.M_s = c.f_shared; g.K_s = c.d;
     g.x_s = x_sh;
     g.out_s = at<char>(ws, L.h_s);
-    g.out_s_lo = at<char>(ws, L.x_perm + (size_t)c.T * c.k * c.f * 2);
     g.w_s[0] = w4_operand(ws1);
     g.w_s[1] = w4_operand(ws3);
   }
@@ -881,13 +877,11 @@ moe_status enqueue_experts_w4(const moe_config& c, int group, const void* x, con
   q.max_rows = g.max_rows;
   q.M = c.d; q.K = c.f;
   q.x = g.out;
-  q.x_lo = g.out_lo;
   q.out = y_perm;
   q.w[0] = w4_operand(w2);
   if (shared) {
     q.dense_rows = c.T; q.M_s = c.d; q.K_s = c.f_shared;
     q.x_s = g.out_s;
-    q.x_s_lo = g.out_s_lo;
     q.out_s = y_sh;
     q.w_s[0] = w4_operand(ws2);
   }

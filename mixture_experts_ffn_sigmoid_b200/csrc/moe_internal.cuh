@@ -263,13 +263,12 @@ struct W4GemmParams {
   int group;                // 32, 64 or 128; divides K and K_s
   int n_routed; const int* offsets; int max_rows;
   int M, K;                 // weight rows per routed expert (a multiple of 32), reduction length
-  const void* x; const int* gather; int gather_rows;   // token rows, or the rows that gather picks
+  // mats = 2: bf16 token rows, or the rows that gather picks, into the
+  // intermediate's 16-bit words; mats = 1: those into bf16 rows.
+  const void* x; const int* gather; int gather_rows;
   void* out;                // [max_rows][M]
   int dense_rows, M_s, K_s; // the shared expert, 0 rows: none
   const void* x_s; void* out_s;
-  // The intermediate is a pair of bf16 values: what the first leaves, in arrays
-  // of the same shape (mats = 2: written, mats = 1: read).
-  const void *x_lo, *x_s_lo; void *out_lo, *out_s_lo;
   W4Operand w[2], w_s[2];
   int has_zero;             // some operand has zero points
   int check;                // check offsets and gather, and write the error word anew

@@ -25,9 +25,13 @@
 // largest magnitude into [2^14, 2^15), the k under the 0x00f0 masks by 1/16
 // besides. fp16's eleven bits hold bf16's eight; only values below 2^-27 of
 // the row's largest lose bits. The intermediate h goes from the first launch to
-// the second as a pair of bf16 values, so that it loses bits only there (2^-11):
-// as one bf16 value it made the result's error 1.4 times its own rounding, up to
-// 1.6 times for narrow experts. A CTA makes them in shared memory when it comes
+// the second in 16 bits a value with fp16's eleven significant ones (2^-11; bf16's
+// eight made the result's error 1.4 times its own rounding, up to 1.6 times for
+// narrow experts): as fp16 over the power of two that brings the largest of
+// eight neighbours into [1, 2), and no magnitude to 2, so that bit 14 of a word
+// stays free. The eight free bits hold that power. Values below 2^-14 of the
+// largest of their eight lose bits (to 2^-25 of it). A CTA makes the rows in
+// shared memory when it comes
 // to a segment, with each group's sum, off which the zero points come: it is
 // where the group's product starts from. The product takes its scale in fp32.
 // No weight is rounded.
@@ -92,6 +96,24 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The intermediate's words: value j of eight neighbours has bit h_bit(j) of their
+// exponent byte (a float's: 0 for none, 255 for an infinity or NaN) in its bit 14.
+__device__ __forceinline__ int h_bit(int j) { return (j >> 1) + (j & 1) * 4; }
+__device__ __forceinline__ uint32_t h_exponent(const uint4& v) {
+  const uint32_t m = 0x40004000u;
+  const uint32_t a = ((v.x & m) >> 14) | ((v.y & m) >> 13) | ((v.z & m) >> 12) | ((v.w & m) >> 11);
+  return (a & 15u) | ((a >> 12) & 0xf0u);
+}
+__device__ __forceinline__ __half2 h_pair(uint32_t w) {   // the two values of a word pair, exponent bits off
+  w &= 0xbfffbfffu;
+  return *reinterpret_cast<const __half2*>(&w);
+}
+// 2^p as a pair of fp16, 0 below fp16's smallest.
+__device__ __forceinline__ __half2 half2_power(int p) {
+  const uint32_t h = p >= -14 ? (uint32_t)(p + 15) << 10 : p >= -24 ? 1u << (p + 24) : 0u;
+  const uint32_t w = h * 0x10001u;
+  return *reinterpret_cast<const __half2*>(&w);
 }
 // The four operand pairs of a word of codes: (c0, c4), 16 (c1, c5), (c2, c6), 16 (c3, c7).
 __device__ __forceinline__ void unpack_w4(uint32_t w, uint32_t (&p)[4]) {
@@ -393,26 +415,27 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
         const int v = p.gather[sg.t0 + r];
         src = v >= 0 && v < p.gather_rows ? v : 0;
       }
-      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s : p.x) +
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(sg.dense ? p.x_s : p.x) +
                                                         src * (size_t)sg.K);
-      const uint4* row_lo =
-          MATS == 1 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(sg.dense ? p.x_s_lo : p.x_lo) +
-                                                     src * (size_t)sg.K)
-                    : nullptr;
       const int n8 = sg.K / 8;
-      uint32_t big = 0;                                  // bf16 magnitudes order like their bits, NaN above infinity
+      // The largest magnitude: of two bf16 a word (they order like their bits, NaN
+      // above infinity), or its exponent, as the intermediate's words have it.
+      uint32_t big = 0;
 #pragma unroll 8
       for (int i = lane; i < n8; i += 32) {
         const uint4 v = row[i];
-        big = __vmaxu2(__vmaxu2(big, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
-                       __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        if (MATS == 1)
+          big = max(big, h_exponent(v));
+        else
+          big = __vmaxu2(__vmaxu2(big, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu)),
+                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, o));
-      const uint32_t top = max(big & 0xffffu, big >> 16);
+      const uint32_t top = MATS == 1 ? big << 7 : max(big & 0xffffu, big >> 16);
       // 2^e top in [2^14, 2^15); e splits in two so that both factors are
       // normal numbers, as does the power that the sums are multiplied by.
-      int e = top >= 0x0080u ? 14 - ((int)(top >> 7) - 127) : 140;
+      int e = MATS == 1 || top >= 0x0080u ? 14 - ((int)(top >> 7) - 127) : 140;
       if (top >= 0x7f80u) e = 0;
       const float f1 = __int_as_float((127 + e / 2) << 23), f2 = __int_as_float((127 + e - e / 2) << 23);
       const int b = 24 - e;
@@ -424,29 +447,38 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
 #pragma unroll 2
       for (int i = (warp % team) * 32 + lane; i < n8_pad; i += 32 * team) {   // whole warps: n8_pad is a multiple of 32
         const uint4 v = i < n8 ? row[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        float x[8], sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[2 * j] = __uint_as_float(w[j] << 16) * f1 * f2;
-          x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * f1 * f2;
-        }
-        if (MATS == 1) {       // the pair, rounded to fp16 for the products and their sum alike
-          const uint4 l = i < n8 ? row_lo[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t wl[4] = {l.x, l.y, l.z, l.w};
+        float sum = 0.0f;
+        if (MATS == 1) {
+          // fp16 already: a product with a power of two, rounded once where it
+          // falls below fp16's normal numbers.
+          const int up = 14 + (int)h_exponent(v) - (int)big;
+          const __half2 f = half2_power(up), f16 = half2_power(up - 4);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 h = __half22float2(__floats2half2_rn(x[2 * j] + __uint_as_float(wl[j] << 16) * f1 * f2,
-                                                              x[2 * j + 1] + __uint_as_float(wl[j] & 0xffff0000u) * f1 * f2));
-            x[2 * j] = h.x;
-            x[2 * j + 1] = h.y;
+            const float2 x = __half22float2(__hmul2(h_pair(w[j]), f));
+            sum += x.x;
+            sum += x.y;
           }
-        }
+          const __half2 o[4] = {__hmul2(h_pair(__byte_perm(v.x, v.z, 0x5410)), f),
+                                __hmul2(h_pair(__byte_perm(v.x, v.z, 0x7632)), f16),
+                                __hmul2(h_pair(__byte_perm(v.y, v.w, 0x5410)), f),
+                                __hmul2(h_pair(__byte_perm(v.y, v.w, 0x7632)), f16)};
+          *reinterpret_cast<uint4*>(to + i * 16) = *reinterpret_cast<const uint4*>(o);
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += x[j];
-        *reinterpret_cast<uint4*>(to + i * 16) =
-            make_uint4(half_pair(x[0], x[4]), half_pair(x[1] * 0.0625f, x[5] * 0.0625f), half_pair(x[2], x[6]),
-                       half_pair(x[3] * 0.0625f, x[7] * 0.0625f));
+          for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(w[j] << 16) * f1 * f2;
+            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * f1 * f2;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum += x[j];
+          *reinterpret_cast<uint4*>(to + i * 16) =
+              make_uint4(half_pair(x[0], x[4]), half_pair(x[1] * 0.0625f, x[5] * 0.0625f), half_pair(x[2], x[6]),
+                         half_pair(x[3] * 0.0625f, x[7] * 0.0625f));
+        }
 #pragma unroll
         for (int o = 1; o < GROUP / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (i % (GROUP / 8) == 0)
@@ -472,26 +504,45 @@ __global__ void __launch_bounds__(W4_THREADS, 2)
     // A finished tile: lane's rows g and g + 8, token columns 2 q and 2 q + 1.
     auto finish = [&](int m) {
       const size_t first = (size_t)sg.t0 * sg.M + m + g;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sg.dense ? p.out_s : p.out) + first;
-      __nv_bfloat16* out_lo = MATS == 2 ? static_cast<__nv_bfloat16*>(sg.dense ? p.out_s_lo : p.out_lo) + first : nullptr;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        if (MATS == 2) {
+          // The activation, by eight neighbours (the lanes of one q): the largest
+          // exponent, of magnitudes raised by 2^-11 so that none rounds up to 2.
+          float v[4];
+          uint32_t ex = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = t * 8 + q * 2 + (i & 1);
-          if (n >= sg.rows) continue;
-          const float2 fac = xfac[n];
-          const float v0 = acc[0][t][i] * fac.x * fac.y, v1 = acc[1][t][i] * fac.x * fac.y;
-          __nv_bfloat16* at = out + (size_t)n * sg.M + (i >> 1) * 8;
-          if (MATS == 2) {     // the activation as a pair: bf16 alone would double the result's error
-            const float v = v0 / (1.0f + __expf(-v0)) * v1;
-            at[0] = __float2bfloat16_rn(v);
-            out_lo[(size_t)n * sg.M + (i >> 1) * 8] = __float2bfloat16_rn(v - __bfloat162float(at[0]));
-          } else {             // the result's one rounding
-            at[0] = __float2bfloat16_rn(v0);
-            at[16] = __float2bfloat16_rn(v1);
+          for (int i = 0; i < 4; ++i) {
+            const float2 fac = xfac[t * 8 + q * 2 + (i & 1)];
+            const float v0 = acc[0][t][i] * fac.x * fac.y, v1 = acc[1][t][i] * fac.x * fac.y;
+            v[i] = v0 / (1.0f + __expf(-v0)) * v1;
+            ex |= ((__float_as_uint(v[i] * (1.0f + 0x1p-11f)) & 0x7fffffffu) >> 23) << (8 * i);
+          }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) ex = __vmaxu4(ex, __shfl_xor_sync(0xffffffffu, ex, o));
+          uint16_t* out = static_cast<uint16_t*>(sg.dense ? p.out_s : p.out) + first;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = t * 8 + q * 2 + (i & 1);
+            if (n >= sg.rows) continue;
+            const uint32_t e = (ex >> (8 * i)) & 255u;
+            const float f = __uint_as_float(e >= 254u ? 0x00400000u : (254u - e) << 23);    // 2^(127 - e)
+            const uint32_t w = __half_as_ushort(__float2half_rn(v[i] * f)) & 0xbfffu;
+            out[(size_t)n * sg.M + (i >> 1) * 8] = (uint16_t)(w | ((e >> h_bit(g)) & 1u) << 14);
+          }
+        } else {
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(sg.dense ? p.out_s : p.out) + first;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {    // the result's one rounding
+            const int n = t * 8 + q * 2 + (i & 1);
+            if (n >= sg.rows) continue;
+            const float2 fac = xfac[n];
+            __nv_bfloat16* at = out + (size_t)n * sg.M + (i >> 1) * 8;
+            at[0] = __float2bfloat16_rn(acc[0][t][i] * fac.x * fac.y);
+            at[16] = __float2bfloat16_rn(acc[1][t][i] * fac.x * fac.y);
           }
         }
+      }
     };
     int c = from % sg.nch, m = (sg.tile0 + from / sg.nch) * WROWS;
     bool began = c == 0;
