@@ -961,11 +961,14 @@ struct NsPlan {
   size_t err, partial, x0, x1, a, b, diag, total;
 };
 
+bool ns_on_chip(int m, int n) { return m <= NSC_M && n <= NSC_N; }
+
 // A matrix is independent of the others; enough of them run together to give
 // the smallest product (tiles of A) about eight rounds of tiles per CTA pair,
-// and no more, so that the scratch stays small and near L2's size.
+// and no more, so that the scratch stays small and near L2's size. Matrices that
+// stay on chip have no scratch but the error word, and run all together.
 NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
-  NsPlan q;
+  NsPlan q = {};
   q.m = rows < cols ? rows : cols;
   q.n = rows < cols ? cols : rows;
   q.ld_x = (q.n + 7) / 8 * 8;
@@ -973,7 +976,8 @@ NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
   const long long t = ceil_div(q.m, 2 * NS_HALF), tiles = t * (t + 1) / 2;
   long long most = ceil_div_ll(8LL * (num_sms / 2), tiles);
   if (most > 32768) most = 32768;
-  const long long rounds = ceil_div_ll(n_mat > 0 ? n_mat : 1, most);
+  const bool chip = ns_on_chip(q.m, q.n);
+  const long long rounds = chip ? 1 : ceil_div_ll(n_mat > 0 ? n_mat : 1, most);
   q.batch = (int)ceil_div_ll(n_mat > 0 ? n_mat : 1, rounds);
   const long long size = (long long)rows * cols, blocks = ceil_div_ll(size, NS_NORM_THREADS * 8 * 4);
   q.norm_blocks = (int)(blocks < NS_NORM_MAX ? blocks : NS_NORM_MAX);
@@ -984,17 +988,17 @@ NsPlan ns_plan(int n_mat, int rows, int cols, int num_sms) {
     return o;
   };
   q.err = take(kNsAlign);
-  q.partial = take((size_t)q.batch * q.norm_blocks * 4);
-  q.x0 = take((size_t)q.batch * q.m * q.ld_x * 2);
-  q.x1 = take((size_t)q.batch * q.m * q.ld_x * 2);
-  q.a = take((size_t)q.batch * q.m * q.ld_a * 2);
-  q.b = take((size_t)q.batch * q.m * q.ld_a * 2);
-  q.diag = take(q.m <= NSC_M ? (size_t)q.batch * q.m * 4 : 0);
+  if (!chip) {
+    q.partial = take((size_t)q.batch * q.norm_blocks * 4);
+    q.x0 = take((size_t)q.batch * q.m * q.ld_x * 2);
+    q.x1 = take((size_t)q.batch * q.m * q.ld_x * 2);
+    q.a = take((size_t)q.batch * q.m * q.ld_a * 2);
+    q.b = take((size_t)q.batch * q.m * q.ld_a * 2);
+    q.diag = take(q.m <= NSC_M ? (size_t)q.batch * q.m * 4 : 0);
+  }
   q.total = off;
   return q;
 }
-
-bool ns_on_chip(int m, int n) { return m <= NSC_M && n <= NSC_N; }
 
 template <typename T, bool MOM>
 cudaError_t launch_ns_chip(const NsChipParams& cp, cudaStream_t s) {
@@ -1052,7 +1056,7 @@ cudaError_t launch_ortho(const OrthoParams& p, void* workspace, int num_sms, cud
     g.m = q.m; g.n = q.n;
     g.ld_x = q.ld_x; g.ld_a = q.ld_a;
     g.a_in = a;
-    g.diag = q.m <= NSC_M ? reinterpret_cast<float*>(ws + q.diag) : nullptr;
+    g.diag = !chip && q.m <= NSC_M ? reinterpret_cast<float*>(ws + q.diag) : nullptr;
     g.tall = p.rows > p.cols;
     g.rows = p.rows; g.cols = p.cols;
     g.o = p.o ? static_cast<__nv_bfloat16*>(p.o) + first * size : nullptr;
