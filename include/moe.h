@@ -548,8 +548,8 @@ MOE_API moe_status moe_w4_dequantize(int64_t rows, int32_t K, int32_t dtype, int
  * MOE_ERR_UNSUPPORTED. The SwiGLU intermediate has fp16's eleven significant bits
  * under a power of two for every eight neighbours (those below 2^-14 of the
  * largest of the eight lose some). Any T is computed; the weights of an expert
- * are read again for every 8 to 32 of its rows, so long batches belong to
- * moe_expert_swiglu. Rows of y_perm that no segment covers are left as they
+ * are read again for every 8 of its rows (16 in long batches with groups of 128,
+ * fewer where rows are very wide), so long batches belong to moe_expert_swiglu. Rows of y_perm that no segment covers are left as they
  * were. A token row with an infinity or NaN gives NaN in its own outputs only.
  * Outputs are distinct arrays; x and x_shared may be one.
  */

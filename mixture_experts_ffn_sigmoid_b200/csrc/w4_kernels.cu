@@ -698,12 +698,6 @@ bool make_w4_tmap(CUtensorMap* tm, const void* q, long long rows, int K) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Experts that a batch is expected to touch under even routing.
-double w4_touched(const W4GemmParams& p) {
-  if (p.n_routed <= 0 || p.max_rows <= 0) return 0.0;
-  return p.n_routed * (1.0 - pow(1.0 - 1.0 / p.n_routed, (double)p.max_rows));
-}
-
 // Shared memory of a CTA that has an SM alone, and of two that share one.
 constexpr int W4_SMEM = 232000, W4_SMEM_HALF = 115000;
 
@@ -732,36 +726,33 @@ struct W4Shape {
   int nt, ctas, smem;
 };
 
-// Token tiles of eight per pass, and CTAs an SM. More token tiles do more
-// products a weight (1, 1.3 and 2 times the time of one), fewer passes over a
-// segment's weights. Token rows that do not fit twice in an SM's shared memory
-// leave one CTA there (1.4 times the time; 12 warps instead of 8 in it gained 2%
-// at 7168-wide rows); those that do not fit at all take fewer rows a pass.
-// Routed segments vary about their mean.
-bool w4_shape(const W4GemmParams& p, W4Shape& best) {
-  const double act = w4_touched(p), cost[3] = {1.0, 1.3, 2.0};
-  double least = 1e300;
-  for (int i = 0; i < 3; ++i) {
-    W4Shape s;
-    s.nt = 1 << i;
-    int rows = 8 * s.nt;
-    while (rows > 1 && w4_layout(p, s.nt, rows, s.plan) > W4_SMEM) rows /= 2;
-    if (s.nt > 1 && rows < 8 * s.nt) break;
-    s.smem = w4_layout(p, s.nt, rows, s.plan);
-    if (s.smem > W4_SMEM) break;
-    s.ctas = s.smem <= W4_SMEM_HALF ? 2 : 1;
-    double t = (double)p.M_s * p.K_s * ceil_div(p.dense_rows, rows);
-    if (act > 0.0) {
-      const double mean = p.max_rows / act, passes = (mean + sqrt(mean)) / rows;
-      t += act * p.M * p.K * (passes > 1.0 ? passes : 1.0);
-    }
-    t *= cost[i] * (s.ctas == 2 ? 1.0 : 1.4);
-    if (t < least) {
-      least = t;
-      best = s;
-    }
-  }
-  return least < 1e300;
+// Eight token rows a pass, or sixteen where groups are of 128 and the segments'
+// rows (their mean, by weights) are 64 at least; fewer where rows that wide do not
+// fit in an SM's shared memory. Two CTAs an SM where their rows fit twice.
+// A second tile of eight shares the unpacking of a weight, but its accumulators
+// leave the warps less to hide latency with, and half of it idles behind a short
+// segment. us, one tile and two, by rows of each expert:
+//                       8         16         32         64         128
+//  64 of 768 x 2048
+//    G 128            60   73    87   85   144  135   264  243   504  463
+//    G 64             62   84    91   96   152  154   281  276   538  526
+//    G 32             67  103    99  116   167  189   309  342   595  655
+//    G 32, zeros      83  158   126  173   214  286   401  523   777 1009
+//  128 of 256 x 512, G 128
+//                     27   32    34   37    51   48    85   73   148  126
+//  8 of 1536 x 4096, G 128
+//                     41   57    63   78    94  107   157  159   284  264
+// Four tiles spill and took 1.3 to 2 times the time of one everywhere.
+bool w4_shape(const W4GemmParams& p, W4Shape& s) {
+  const double routed = p.n_routed * (double)p.M * p.K, shared = p.dense_rows > 0 ? (double)p.M_s * p.K_s : 0.0;
+  const double weighted = (double)p.max_rows * p.M * p.K + shared * p.dense_rows;   // rows of a segment x its weights
+  s.nt = p.group == 128 && weighted >= 64.0 * (routed + shared) ? 2 : 1;
+  if (s.nt == 2 && w4_layout(p, 2, 16, s.plan) > W4_SMEM) s.nt = 1;
+  int rows = 8 * s.nt;
+  while (rows > 1 && w4_layout(p, s.nt, rows, s.plan) > W4_SMEM) rows /= 2;
+  s.smem = w4_layout(p, s.nt, rows, s.plan);
+  s.ctas = s.smem <= W4_SMEM_HALF ? 2 : 1;
+  return s.smem <= W4_SMEM;
 }
 
 // ------------------------------------------------------ making the weights
@@ -952,18 +943,19 @@ cudaError_t launch_w4_gemm(const W4GemmParams& p, int num_sms, cudaStream_t s) {
   auto with = [&](auto mats, auto n, auto zero) {
     constexpr int M = decltype(mats)::value, N = decltype(n)::value;
     constexpr bool Z = decltype(zero)::value;
-    return p.group == 128  ? go(KernelTag<w4_gemm_kernel<M, N, 128, Z>>{})
-           : p.group == 64 ? go(KernelTag<w4_gemm_kernel<M, N, 64, Z>>{})
-                           : go(KernelTag<w4_gemm_kernel<M, N, 32, Z>>{});
+    if constexpr (N == 2)      // groups of 128 only
+      return go(KernelTag<w4_gemm_kernel<M, N, 128, Z>>{});
+    else
+      return p.group == 128  ? go(KernelTag<w4_gemm_kernel<M, N, 128, Z>>{})
+             : p.group == 64 ? go(KernelTag<w4_gemm_kernel<M, N, 64, Z>>{})
+                             : go(KernelTag<w4_gemm_kernel<M, N, 32, Z>>{});
   };
   auto mats = [&](auto n, auto zero) {
     return p.mats == 2 ? with(std::integral_constant<int, 2>{}, n, zero)
                        : with(std::integral_constant<int, 1>{}, n, zero);
   };
   auto rows_of = [&](auto n) { return p.has_zero ? mats(n, std::true_type{}) : mats(n, std::false_type{}); };
-  return shape.nt == 1   ? rows_of(std::integral_constant<int, 1>{})
-         : shape.nt == 2 ? rows_of(std::integral_constant<int, 2>{})
-                         : rows_of(std::integral_constant<int, 4>{});
+  return shape.nt == 1 ? rows_of(std::integral_constant<int, 1>{}) : rows_of(std::integral_constant<int, 2>{});
 }
 
 cudaError_t launch_w4_quantize(int dtype, const void* w, long long n, int group, void* q, void* scale, void* zero,

@@ -88,3 +88,12 @@ def test_an_intermediate_that_overflows_stays_in_its_row():
     assert torch.equal(out[~hit], y[~hit]) and torch.isnan(out[hit].float()).all()
     rest = torch.arange(9, device="cuda") != 4
     assert torch.equal(outs[rest], ys[rest]) and torch.isnan(outs[4].float()).all()
+
+
+@pytest.mark.parametrize("T,d,E,k,f,fs,zeros", [
+    (200, 256, 3, 1, 256, 128, False), (197, 384, 3, 1, 128, 0, True), (71, 512, 2, 2, 384, 128, True),
+    (64, 128, 1, 1, 128, 0, False), (77, 16384, 1, 1, 128, 128, False), (65, 128, 1, 1, 16384, 0, True)])
+def test_sixteen_rows_a_pass(T, d, E, k, f, fs, zeros):
+    # Groups of 128 and 64 rows a segment or more; the widest rows fit eight or fewer at a time.
+    a = W.make(T, d, E, k, f, fs, 128, zeros, seed=31)
+    check(*a, *W.run_experts(*a))
