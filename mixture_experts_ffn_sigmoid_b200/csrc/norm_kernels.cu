@@ -31,11 +31,13 @@
 // the second of one row and the first of the next share a barrier.
 //
 // Measured, bf16, T = 4096, d = 7168: forward 45 us (235 MB: 5.2 TB/s, 79% of
-// the copy rate; 69% of the issue slots), backward 80 us and 6 for the sums over
-// runs (353 MB: 4.1 TB/s; a row's four vectors a thread and the sums leave 14
-// warps an SM, which issue in 55% of the cycles). fp32, T = 1111, d = 1000:
-// backward 16.8 us, two launches' latency more than their 27 MB. 32 rows of
-// 2048: 3.8 us on the GPU.
+// the copy rate; 69% of the issue slots), backward 77 us (353 MB: 4.6 TB/s, 70%),
+// 72 of them the rows, 5 the sums over runs (a row's four vectors a thread and the
+// sums leave 14 warps an SM, which issue in 62% of the cycles). 4096 x 4096: 31
+// and 54 us. Five vectors a thread spill: 4096 x 8192 takes 174 and 296 us, fp32
+// 4096 x 4096 126 and 149. fp32, T = 1111, d = 1000: backward 16.4 us, 15.1 on the
+// GPU, for 27 MB: 371 runs of three rows and the sums over them. 32 rows of 2048:
+// 3.5 us on the GPU.
 //
 // Weight gradients: in the backward each CTA takes a contiguous run of rows
 // and keeps fp32 sums (dw_pre's and the gate's in registers, dw_post's, which
@@ -48,8 +50,10 @@
 namespace moe {
 namespace {
 
-// Two 16-byte vectors a thread up to 14 KB rows, then five: 448 threads leave
-// 73 registers each to two CTAs an SM, 146 to one.
+// Two 16-byte vectors a thread up to 14 KB rows, then five. 448 threads leave 72
+// registers each to two CTAs an SM; one CTA's get 128. Two vectors fit those (20
+// bytes spilled in the bf16 forward), five do not: 0.6 KB a thread spilled in the
+// bf16 forward, 1.1 in the backward, 0.2 in fp32.
 constexpr int kNormMaxThreads = 448;
 constexpr int kNormWideVpt = 5;
 constexpr int kNormMaxStages = 4;

@@ -41,9 +41,10 @@
 // stored once. The last step's epilogue writes the result or the weights.
 //
 // Measured, five steps: 8 x 2048 x 7168 as a Muon step in bf16 3.6 to 4.3 ms with
-// the power cap (3.95 TFLOP: 0.92 to 1.1 PFLOP/s; the products alone run at 1.33,
-// 1.02 and 1.36 PFLOP/s for A, B and X, the two first passes take 317 us for
-// their 2.1 GB); 2 x 14336 x 4096 6.9 to 7.4 ms (1.1 PFLOP/s). Middling matrices
+// the power cap (3.95 TFLOP: 0.92 to 1.1 PFLOP/s; launched one by one the products
+// take 207, 76 and 366 us for A, B and X, the last one 401, at 1.31, 1.01 and 1.31
+// PFLOP/s of the tiles they compute, the two first passes 318 us for their 2.1 GB:
+// 3.6 ms in all); 2 x 14336 x 4096 6.9 to 7.4 ms (1.1 PFLOP/s). Middling matrices
 // are bound by their 15 dependent products: 4 of 256 x 384 take 94 us, of which a
 // product's loads, its way out of TMEM and the stores' way to the next one are
 // 1.5 to 2 us each. One launch for all

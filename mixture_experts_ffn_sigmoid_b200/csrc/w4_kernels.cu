@@ -31,13 +31,12 @@
 // eight neighbours into [1, 2), and no magnitude to 2, so that bit 14 of a word
 // stays free. The eight free bits hold that power. Values below 2^-14 of the
 // largest of their eight lose bits (to 2^-25 of it). A CTA makes the rows in
-// shared memory when it comes
-// to a segment, with each group's sum, off which the zero points come: it is
-// where the group's product starts from. The product takes its scale in fp32.
-// No weight is rounded.
+// shared memory when it comes to a segment, with each group's sum, off which the
+// zero points come: it is where the group's product starts from. The product
+// takes its scale in fp32. No weight is rounded.
 //
 // Layout of the work: the tiles of all non-empty segments (16 rows of W1 and W3,
-// or 32 rows of W2, with up to 8 NT of the segment's token rows) are dealt to
+// or 32 rows of W2, with a pass's 8 or 16 of the segment's token rows) are dealt to
 // the CTAs in contiguous runs of equal length, so a batch that touches few
 // experts still uses every SM. Within a CTA a run is cut where the token rows
 // change; the chunks (256 k) of each piece's tiles go to its 8 warps in equal
@@ -49,13 +48,17 @@
 // flow all the time. What is left to the lanes per 1024 weights (32 k of two
 // tiles) is 5 shared reads, 20 integer instructions and 4 products.
 //
-// Measured: 32 tokens, 128 experts of 768 x 2048, top 8 (273 MB of weights and
-// rows): 58 us the two launches in one stream, 4.7 TB/s, 72% of the copy
-// rate; gate/up alone 39.9 us with half of the issue slots taken and the
-// integer pipe at 54%. 1 token: 16.6 us, most of it two launches' start and the
-// first loads. 24 tokens, 32 experts of 2048 x 7168 and the shared one, groups
-// of 64 with zero points (797 MB): 302 us, 2.6 TB/s: its token rows (115 KB)
-// leave one CTA an SM, whose 8 warps issue in 46% of the cycles.
+// Measured: 32 tokens, 128 experts of 768 x 2048, top 8, of which 72 are touched
+// (176 MB of weights and rows): 58 to 60 us the two launches in one stream, 3.0
+// TB/s, 46% of the copy rate. Nothing is full: gate/up alone takes 42 us with the
+// issue slots at 51%, the integer pipe at 54%, the tensor pipe at 20% and DRAM at
+// 35%; its warps, with one chunk each in flight, wait most for their own chains of
+// unpacking and products. 1 token (19.5 MB): 16.9 us, most of it two launches'
+// start and the first loads. 24 tokens, 32 experts of 2048 x 7168 and the shared
+// one, groups of 64 with zero points (798 MB): 282 to 302 us, 2.7 TB/s: gate/up's
+// token rows (115 KB) leave one CTA an SM, whose 8 warps issue in 46% of the
+// cycles, and it reads 633 MB, as segments of more than eight rows stream their
+// weights twice.
 #include <cuda_fp16.h>
 
 #include <type_traits>
