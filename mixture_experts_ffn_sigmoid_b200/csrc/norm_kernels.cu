@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1)
       const float cy = post ? ry * (ry * s[3] * inv_d) : 0.0f;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        float f[N], o[N];
-        unpack16<T>(ring.get(slot, 1, j), f);
+        float f[N] = {}, o[N];
+        if (post) unpack16<T>(ring.get(slot, 1, j), f);   // without a norm no y: it may be infinite
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = ry * fmaf(-cy, f[i], dm[j][i]);
         if (tid + j * nt < nv) static_cast<uint4*>(p.dy)[off + j * nt] = pack16<T>(o);

@@ -94,3 +94,16 @@ def test_as_many_tokens_as_an_int_counts(T, gt, freed):
     room = torch.zeros(gates, d, device="cuda", dtype=torch.float64).index_add_(0, rows // gt, want["dgate"].double().abs())
     # Each token's part was rounded to bf16 above, and the sum is here, off by 2^-8 of what it came to.
     assert ((dg.double() - by_gate).abs() <= 2 ** -8 * (room + by_gate.abs() + 2 ** -8 * room) + 1e-30).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "f32"), (2048, "bf16"), (8200, "bf16"), (16384, "bf16")])
+def test_a_branch_without_a_norm_passes_its_gradient_whatever_its_values(d, dtype):
+    # dy = beta gate dh' then: no value of y enters it, nor dh.
+    cfg, dt, t, (_, dh) = N.make(12, d, dtype, 3, post=False, pre=False, alpha=0.5, beta=2.0)
+    h_out, _ = N.forward(cfg, dt, t)
+    o = N.backward(cfg, dt, t, None, dh, h_out, dgate=1)
+    N.check_backward(cfg, dt, t, None, dh, h_out, o)
+    y = t["y"].clone()
+    y[2, 5], y[7, 0], y[9] = float("inf"), float("nan"), -float("inf")
+    o2 = N.backward(cfg, dt, dict(t, y=y), None, dh, h_out, dgate=1)
+    assert torch.equal(o2["dy"], o["dy"]) and torch.equal(o2["dh"], o["dh"])
