@@ -31,7 +31,7 @@
 // the second of one row and the first of the next share a barrier.
 //
 // Measured, bf16, T = 4096, d = 7168: forward 45 us (235 MB: 5.2 TB/s, 79% of
-// the copy rate; 69% of the issue slots), backward 77 us (353 MB: 4.6 TB/s, 70%),
+// the copy rate; 69% of the issue slots), backward 77 to 78 us (353 MB: 4.6 TB/s, 70%),
 // 72 of them the rows, 5 the sums over runs (a row's four vectors a thread and the
 // sums leave 14 warps an SM, which issue in 62% of the cycles). 4096 x 4096: 31
 // and 54 us. Five vectors a thread spill: 4096 x 8192 takes 174 and 296 us, fp32

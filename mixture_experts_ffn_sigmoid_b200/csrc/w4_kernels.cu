@@ -49,13 +49,13 @@
 // tiles) is 5 shared reads, 20 integer instructions and 4 products.
 //
 // Measured: 32 tokens, 128 experts of 768 x 2048, top 8, of which 72 are touched
-// (176 MB of weights and rows): 58 to 60 us the two launches in one stream, 3.0
+// (176 MB of weights and rows): 58 to 61 us the two launches in one stream, 3.0
 // TB/s, 46% of the copy rate. Nothing is full: gate/up alone takes 42 us with the
 // issue slots at 51%, the integer pipe at 54%, the tensor pipe at 20% and DRAM at
 // 35%; its warps, with one chunk each in flight, wait most for their own chains of
 // unpacking and products. 1 token (19.5 MB): 16.9 us, most of it two launches'
 // start and the first loads. 24 tokens, 32 experts of 2048 x 7168 and the shared
-// one, groups of 64 with zero points (798 MB): 282 to 302 us, 2.7 TB/s: gate/up's
+// one, groups of 64 with zero points (798 MB): 282 to 308 us, 2.7 TB/s: gate/up's
 // token rows (115 KB) leave one CTA an SM, whose 8 warps issue in 46% of the
 // cycles, and it reads 633 MB, as segments of more than eight rows stream their
 // weights twice.
